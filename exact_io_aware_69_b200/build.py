@@ -1,4 +1,4 @@
-"""Build the CUDA library libfa.so in-tree (sm_100a only).
+"""Build the CUDA libraries libfa.so and libfa_paged.so in-tree (sm_100a only).
 
 ``python -m exact_io_aware_69_b200.build`` or ``build_library()``. The CUDA runtime is
 linked statically and the driver entry point for TMA descriptors is fetched at run
@@ -25,6 +25,17 @@ SOURCES = [os.path.join(CSRC, "fa_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
     os.path.join(INCLUDE, "fa.h")]
 
+# The rotary and paged-cache library: a translation unit of its own that shares
+# sm100.cuh and fa_band.cuh with the first.
+CSRC_PAGED = os.path.join(PKG, "csrc_paged")
+PAGED_LIB = os.path.join(PKG, "libfa_paged.so")
+PAGED_RESOURCES = os.path.join(PKG, "libfa_paged.resources.json")
+PAGED_SOURCES = [os.path.join(CSRC_PAGED, "fa_paged_api.cu")]
+PAGED_DEPS = PAGED_SOURCES + [
+    os.path.join(CSRC_PAGED, f) for f in os.listdir(CSRC_PAGED) if f.endswith(".cuh")] + [
+    os.path.join(CSRC, f) for f in ("sm100.cuh", "fa_band.cuh")] + [
+    os.path.join(INCLUDE, f) for f in ("fa.h", "fa_paged.h")]
+
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
@@ -38,11 +49,15 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(lib: str, deps) -> bool:
+    if not os.path.exists(lib):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in DEPS if os.path.exists(p))
+    t = os.path.getmtime(lib)
+    return all(os.path.getmtime(p) <= t for p in deps if os.path.exists(p))
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, DEPS)
 
 
 def parse_ptxas_report(text: str) -> dict:
@@ -80,11 +95,9 @@ def check_resources(report: dict) -> None:
                                    f"thread; its register split needs exactly {regs}")
 
 
-def build_library(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date() and os.path.exists(RESOURCES):
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, "-Xptxas", "-v", "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", tmp]
+def _compile(lib: str, sources, resources: str, verbose: bool) -> None:
+    tmp = lib + f".tmp{os.getpid()}"
+    cmd = [nvcc(), *NVCC_FLAGS, "-Xptxas", "-v", "-I", INCLUDE, "-I", CSRC, *sources, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
@@ -96,17 +109,32 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     except RuntimeError:
         os.unlink(tmp)
         raise
-    with open(RESOURCES + ".tmp", "w") as fh:
+    with open(resources + ".tmp", "w") as fh:
         json.dump(report, fh, indent=1, sort_keys=True)
-    os.replace(RESOURCES + ".tmp", RESOURCES)
-    os.replace(tmp, LIB)
+    os.replace(resources + ".tmp", resources)
+    os.replace(tmp, lib)
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Build what is out of date (force: everything); returns libfa.so's path."""
+    if force or not (up_to_date() and os.path.exists(RESOURCES)):
+        _compile(LIB, SOURCES, RESOURCES, verbose)
+    if force or not (_newer(PAGED_LIB, PAGED_DEPS) and os.path.exists(PAGED_RESOURCES)):
+        _compile(PAGED_LIB, PAGED_SOURCES, PAGED_RESOURCES, verbose)
     return LIB
 
 
 def resources() -> dict:
-    """ptxas's report of the current build (builds first when it is missing)."""
+    """ptxas's report of the current libfa.so (builds first when it is missing)."""
     build_library()
     with open(RESOURCES) as fh:
+        return json.load(fh)
+
+
+def paged_resources() -> dict:
+    """ptxas's report of the current libfa_paged.so."""
+    build_library()
+    with open(PAGED_RESOURCES) as fh:
         return json.load(fh)
 
 

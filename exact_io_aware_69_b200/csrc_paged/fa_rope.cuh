@@ -1,0 +1,195 @@
+// fa_rope.cuh -- rotary positions, and the append of new tokens to a paged cache with the
+// rotation applied on the way: one kernel, since both move rows of heads once and turn
+// some of them.
+//
+// Pair i of a row at position pos is turned by a = pos * freqs[i]. The product and its
+// reduction by whole turns are 64-bit (at pos = 10^6 a 32-bit product is off by 0.06 rad);
+// sine and cosine of the reduced angle, the rotation and the magnitude are 32-bit, and the
+// result is rounded once to 16 bits.
+//
+// The pass is bound by HBM: every element is read and written once. So a block takes a few
+// tokens, computes their rot_dim / 2 sines and cosines once into shared memory (a token's
+// angles serve all its heads; per thread and head they would cost more instructions than
+// the rotation), and its threads then stream rows: a thread owns 16 columns of a row as two
+// 16-byte vectors (the two halves of eight pairs in the half form, 16 neighbours in the
+// interleaved form, or 16 columns that are copied) and keeps their angles in registers over
+// the heads of its token. kRopeRows rows are loaded before the first is stored.
+#pragma once
+
+#include "fa_paged_common.cuh"
+
+namespace fa {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeRows = 4;          // rows in flight per thread
+constexpr int kRopeMaxTokens = 8;     // tokens of a block
+constexpr int kRopeMaxDim = 1024;
+
+struct RopeRows {
+  const uint16_t* src;
+  uint16_t* dst;
+  Strides ss, sd;
+  int heads;
+};
+
+struct RopeArgs {
+  RopeRows q, k, v;  // v: rows that are copied (append only)
+  const int* positions;
+  long pos_row;
+  const double* freqs;
+  int rot, d;
+  float magnitude, sign;  // sign: -1 turns back
+  int N;                  // rows per batch (rope), packed rows (append: one batch)
+  long rows;              // B * N
+  int tokens_per_block;
+  PagedView cache;        // append only; its pages are the destination of k and v
+};
+
+__device__ __forceinline__ void sincos_of(int pos, double freq, float* s, float* c) {
+  const double turns2 = static_cast<double>(pos) * freq * 0.31830988618379067154;  // angle / pi
+  const double r = turns2 - 2.0 * rint(0.5 * turns2);                             // in [-1, 1]
+  sincospif(static_cast<float>(r), s, c);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void rotate16(uint4& a, uint4& b, const float* cs, const float* sn,
+                                         bool interleaved) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (interleaved) {  // pair i in word i
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float x0, x1;
+      unpack2<BF16>(w[i], x0, x1);
+      w[i] = pack2<BF16>(x0 * cs[i] - x1 * sn[i], x1 * cs[i] + x0 * sn[i]);
+    }
+  } else {  // pair i: value i of the first vector with value i of the second
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x0, x1, y0, y1;
+      unpack2<BF16>(w[i], x0, y0);
+      unpack2<BF16>(w[4 + i], x1, y1);
+      const int p = 2 * i;
+      w[i] = pack2<BF16>(x0 * cs[p] - x1 * sn[p], y0 * cs[p + 1] - y1 * sn[p + 1]);
+      w[4 + i] = pack2<BF16>(x1 * cs[p] + x0 * sn[p], y1 * cs[p + 1] + y0 * sn[p + 1]);
+    }
+  }
+  a = make_uint4(w[0], w[1], w[2], w[3]);
+  b = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <bool PAGED, bool BF16>
+__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a,
+                                                               const bool interleaved) {
+  extern __shared__ __align__(16) float rope_smem[];  // [tokens][rot / 2] cos, then sin
+  __shared__ int s_pos[kRopeMaxTokens];
+  __shared__ int s_owner[kRopeMaxTokens];  // append: -1 = the token belongs to nobody
+  __shared__ int s_page[kRopeMaxTokens];   // append: destination page (-1: not written)
+  __shared__ int s_row[kRopeMaxTokens];
+
+  const int tpb = a.tokens_per_block;
+  const long t0 = static_cast<long>(blockIdx.x) * tpb;
+  const int nt = static_cast<int>(min(static_cast<long>(tpb), a.rows - t0));
+  const int half = a.rot / 2;
+  float* cosines = rope_smem;
+  float* sines = rope_smem + tpb * half;
+
+  if constexpr (PAGED) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = warp; i < nt; i += kRopeThreads / 32) {
+      const PagedView& c = a.cache;
+      const int t = static_cast<int>(t0) + i;
+      const int b = owner_of(c.cu_q, c.batch, t, lane);
+      if (lane == 0) {
+        int owner = -1, page = -1, row = 0, pos = 0;
+        if (b >= 0 && t < c.cu_q[c.batch]) {
+          const SeqInfo s = seq_info(c, b, c.tokens);
+          pos = s.nk - s.n + (t - s.begin);
+          if (s.ok && s.n <= s.nk && t < s.begin + s.n) {
+            owner = b;
+            page = c.table[static_cast<long>(b) * c.table_row + (pos >> c.page_shift)];
+            row = pos & ((1 << c.page_shift) - 1);
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_pages)) page = -1;
+          }
+          if (owner < 0 || page < 0) atomicExch(&g_fa_status, kStatusInvalid);
+        }
+        s_owner[i] = owner;
+        s_page[i] = page;
+        s_row[i] = row;
+        s_pos[i] = a.positions != nullptr && owner >= 0 ? a.positions[t] : pos;
+      }
+    }
+  } else {
+    if (threadIdx.x < nt) {
+      const long t = t0 + threadIdx.x;
+      const long b = t / a.N;
+      const int n = static_cast<int>(t - b * a.N);
+      s_pos[threadIdx.x] = a.positions != nullptr ? a.positions[b * a.pos_row + n] : n;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+    float s, c;
+    sincos_of(s_pos[i / half], a.freqs[i % half], &s, &c);
+    cosines[i] = c * a.magnitude;
+    sines[i] = s * a.magnitude * a.sign;
+  }
+  __syncthreads();
+
+  // thread = (token, row lane, group of 16 columns), groups fastest
+  const int groups = a.d / 16;
+  const int rlanes = kRopeThreads / groups / tpb;  // threads' rows of one token per pass
+  const int g = threadIdx.x % groups;
+  const int rest = threadIdx.x / groups;
+  const int ti = rest / rlanes;
+  const int rl = rest - ti * rlanes;
+  if (ti >= nt) return;
+  if (PAGED && s_owner[ti] < 0) return;
+  const long t = t0 + ti;
+  const long b = PAGED ? 0 : t / a.N;
+  const long n = PAGED ? t : t - b * a.N;
+  const bool turns = g < a.rot / 16;
+  // first column of the group's two vectors
+  const int c0 = !turns || interleaved ? 16 * g : 8 * g;
+  const int c1 = !turns || interleaved ? c0 + 8 : c0 + half;
+  float cs[8], sn[8];
+  if (turns) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = cosines[ti * half + 8 * g + i];
+      sn[i] = sines[ti * half + 8 * g + i];
+    }
+  }
+  const int nq = a.q.heads, nk = nq + a.k.heads, total = nk + a.v.heads;
+  // rows of K and V whose page is not valid are not written
+  const int last = PAGED && s_page[ti] < 0 ? nq : total;
+  for (int r0 = rl; r0 < last; r0 += kRopeRows * rlanes) {
+    uint4 x[kRopeRows], y[kRopeRows];
+    uint16_t* dst[kRopeRows];
+#pragma unroll
+    for (int u = 0; u < kRopeRows; ++u) {
+      const int r = r0 + u * rlanes;
+      if (r < last) {
+        const RopeRows& rows = r < nq ? a.q : r < nk ? a.k : a.v;
+        const int h = r < nq ? r : r < nk ? r - nq : r - nk;
+        const uint16_t* src = rows.src + b * rows.ss.sb + h * rows.ss.sh + n * rows.ss.sn;
+        x[u] = *reinterpret_cast<const uint4*>(src + c0);
+        y[u] = *reinterpret_cast<const uint4*>(src + c1);
+        // append: K and V rows go to row s_row of page s_page (sb: the page stride)
+        dst[u] = PAGED && r >= nq ? rows.dst + s_page[ti] * rows.sd.sb + h * rows.sd.sh +
+                                        s_row[ti] * rows.sd.sn
+                                  : rows.dst + b * rows.sd.sb + h * rows.sd.sh + n * rows.sd.sn;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRopeRows; ++u) {
+      const int r = r0 + u * rlanes;
+      if (r < last) {
+        if (turns && r < nk) rotate16<BF16>(x[u], y[u], cs, sn, interleaved);
+        *reinterpret_cast<uint4*>(dst[u] + c0) = x[u];
+        *reinterpret_cast<uint4*>(dst[u] + c1) = y[u];
+      }
+    }
+  }
+}
+
+}  // namespace fa

@@ -1,0 +1,119 @@
+/*
+ * fa_paged.h -- C ABI of libfa_paged.so: rotary positions, a paged key/value cache and
+ * exact attention over it, for B200 (sm_100a). It stands beside fa.h: the same status
+ * codes, 16-bit types, masks and ownership rules, in a library of its own.
+ *
+ * Rotary positions. The first rot_dim columns of a head are r/2 pairs (r = rot_dim), pair
+ * i being columns (i, i + r/2) in the half form and (2 i, 2 i + 1) in the interleaved
+ * form. A row at position pos turns pair i by the angle a = pos * freqs[i]:
+ *     y0 = magnitude * (x0 cos a - x1 sin a),   y1 = magnitude * (x1 cos a + x0 sin a);
+ * the other columns are copied. The angle is formed in 64 bits, the rotation in 32, and
+ * the result is rounded once.
+ *
+ * Paged cache. Key j of sequence b is row j % page_size of page table[b][j / page_size];
+ * K and V have pages of the same shape in two arrays with their own strides (so both may
+ * be views of one pool). Tokens of a ragged batch are packed: sequence b owns the rows
+ * cu_q[b] .. cu_q[b+1] - 1 of Q, K, V and O, its n = cu_q[b+1] - cu_q[b] new tokens, and
+ * holds seq_k[b] cached keys, the new tokens included as its last n. Rows behind
+ * cu_q[batch] belong to no sequence and are neither read nor written.
+ *
+ * Masks are fa.h's: with off = seq_k[b] - n, query i of a sequence sees key j iff
+ * i + off - window_left <= j <= i + off + window_right (negative edge: unbounded);
+ * (-1, 0) is causal. Query head h reads key head h / (Hq / heads). A row that sees no key
+ * gets O = 0 and L = -inf. V rows that no query of the attention tile at hand sees are
+ * never multiplied, whatever they hold; keys that some of them see must be finite.
+ *
+ * Lengths, tables and positions are read on the device, so a captured graph follows what
+ * they hold when it runs. What the host cannot check is checked there: a sequence whose
+ * lengths are inconsistent (cu_q decreasing or above the packed rows, more keys than the
+ * table's width holds, fewer keys than new tokens in an append) is left out, and a page
+ * index outside [0, num_pages) reads as zeros and is not written; either makes the next
+ * fa_paged_device_status return FA_ERR_INVALID.
+ *
+ * Pointers are device pointers of the current device, 16-byte aligned (4 for the 32-bit
+ * integer arrays, 8 for freqs); strides are in elements, the last dimension is dense, and
+ * the other strides are multiples of 8 elements. Every call only enqueues work on
+ * `stream`. The caller owns every buffer; two calls that may run at the same time need
+ * workspaces of their own.
+ */
+#ifndef FA_PAGED_H_
+#define FA_PAGED_H_
+
+#include <stddef.h>
+
+#include "fa.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element strides of a [B][H][N][d] tensor in whatever order it lies in memory. */
+typedef struct {
+    long long b, h, n;
+} fa_strides;
+
+typedef struct {
+    void *k_pages;                     /* page p, head h, row j: p*k_page + h*k_head + j*k_row */
+    void *v_pages;
+    long long k_page, k_head, k_row;   /* element strides */
+    long long v_page, v_head, v_row;
+    const int *table;                  /* [batch][table_row], the first table_width used */
+    const int *cu_q;                   /* [batch + 1] */
+    const int *seq_k;                  /* [batch] */
+    int table_row, table_width;
+    int num_pages, page_size;          /* page_size: a power of two, 16 .. 1024 */
+    int heads, d;                      /* key heads; d = 64 or 128 (append: see there) */
+    int batch, tokens;                 /* sequences; packed rows that Q, K, V, O have */
+    int dtype;                         /* FA_BF16 or FA_FP16 */
+} fa_paged_cache;
+
+/*
+ * Rotates Q [B][Hq][N][d] and, with Hk > 0, K [B][Hk][N][d] in one launch; `inverse` = 1
+ * turns by -a instead, which is the gradient of the rotation (same magnitude). Row n of
+ * batch b is at positions[b * pos_row + n] (pos_row = 0: the same for every batch), or at
+ * n when positions is NULL. Y may be X with the same strides (in place); otherwise they
+ * must not overlap. d and rot_dim are multiples of 16, 16 <= rot_dim <= d <= 1024.
+ */
+int fa_rope(const void *Xq, const fa_strides *xq, void *Yq, const fa_strides *yq, int Hq,
+            const void *Xk, const fa_strides *xk, void *Yk, const fa_strides *yk, int Hk,
+            const int *positions, long long pos_row, const double *freqs, int rot_dim,
+            float magnitude, int interleaved, int inverse, int B, int N, int d, int dtype,
+            void *stream);
+
+/*
+ * Writes the new tokens' keys and values, K and V [tokens][heads][d] (strides h and n of
+ * xk, xv), into their pages: V as it is, K rotated (freqs not NULL) or as it is (freqs
+ * NULL). Token i of a sequence takes position seq_k[b] - n + i; `positions` [tokens], if
+ * given, replaces it in the rotation only. With Hq > 0 it also rotates Q [tokens][Hq][d]
+ * into Yq (which may be Xq) in the same launch; that needs freqs. Here d is any multiple
+ * of 16 up to 1024. Tokens of sequences that share a page row race for it.
+ */
+int fa_paged_append(const fa_paged_cache *cache, const void *K, const fa_strides *xk,
+                    const void *V, const fa_strides *xv, const void *Xq, const fa_strides *xq,
+                    void *Yq, const fa_strides *yq, int Hq, const int *positions,
+                    const double *freqs, int rot_dim, float magnitude, int interleaved,
+                    void *stream);
+
+/*
+ * Exact attention of the packed queries Q [tokens][Hq][d] (strides h and n of xq) over
+ * the cache: O [tokens][Hq][d] and L [Hq][tokens] (fp32, natural log). Hq is a multiple of
+ * cache->heads, Hq / heads <= 128. max_q bounds the new tokens of any sequence (one with
+ * more is left out, as above); it picks the kernel. Work is shared out evenly over the
+ * SMs by key tiles, so a sequence's keys may be split between CTAs; the parts are joined
+ * by their log-sum-exps in a fixed order, and results are the same on every call.
+ */
+size_t fa_paged_workspace_size(int tokens, int max_q, int Hq, int heads, int d);
+int fa_paged_attention(const fa_paged_cache *cache, const void *Q, const fa_strides *xq, void *O,
+                       const fa_strides *xo, float *L, int Hq, int max_q, int window_left,
+                       int window_right, float scale, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* fa_get_device_status for the kernels of this library: synchronises `stream`, returns
+ * and clears the current device's error word (FA_ERR_INVALID: see above). */
+int fa_paged_device_status(void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FA_PAGED_H_ */
