@@ -5,9 +5,13 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "fa_paged.h"
 #include "fa_paged_common.cuh"
+#include "fa_paged_merge.cuh"
 #include "fa_paged_simple.cuh"
+#include "fa_paged_step.cuh"
 #include "fa_rope.cuh"
 
 namespace {
@@ -101,21 +105,173 @@ fa::PagedView view_of(const fa_paged_cache& c) {
 // An edge that bounds nothing becomes fa::kUnbounded.
 int edge(int w) { return w < 0 || w >= fa::kUnbounded ? fa::kUnbounded : w; }
 
+// ----------------------------------------------------------------- attention
+// CTAs of an attention launch: one per SM of a B200. A fixed count keeps the split -- and
+// so the rounding where parts are joined -- the same everywhere.
+constexpr int kGrid = 148;
+constexpr size_t kMaxDynSmem = 232448;  // 227 KB per block on sm_100
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+// A 16-bit tensor of four dimensions (columns first, dense) with element strides of the
+// other three; boxes of 64 columns x box1 x box2, 128-byte swizzle, zeros outside.
+bool make_tmap(CUtensorMap* map, const void* ptr, int dtype, const long long (&dims)[4],
+               const long long (&elems)[3], int box1, int box2) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  cuuint64_t size[4], strides[3];
+  for (int i = 0; i < 4; ++i) size[i] = static_cast<cuuint64_t>(dims[i]);
+  // a dimension of one is never stepped over: any valid stride does
+  for (int i = 0; i < 3; ++i)
+    strides[i] = static_cast<cuuint64_t>(dims[i + 1] == 1 ? dims[0] : elems[i]) * 2;
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return enc(map,
+             dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             4, const_cast<void*>(ptr), size, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// A stride of 0 over more than one row would alias rows of a tensor map.
+bool steps(long long stride, long long rows) { return rows <= 1 || stride > 0; }
+
+// Rows (tokens x query heads of a key head) that the step kernel takes for one pass.
+constexpr int kStepMaxRows = 64;
+
+// Workspace: a PartInfo per CTA, then base-2 log-sum-exps and normalised outputs (fp32) of
+// two parts per CTA, `rows` rows each.
+struct Workspace {
+  int rows;
+  size_t l_at, o_at, bytes;
+};
+Workspace workspace_for(int max_q, int group, int d) {
+  Workspace w;
+  const long long rows = static_cast<long long>(max_q) * group;
+  w.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kStepMaxRows ? 64 : 256;
+  w.l_at = kGrid * sizeof(fa::PartInfo);
+  w.o_at = w.l_at + 2ull * kGrid * w.rows * sizeof(float);
+  w.bytes = w.o_at + 2ull * kGrid * w.rows * d * sizeof(float);
+  return w;
+}
+
+struct AttentionArgs {
+  const fa_paged_cache* c;
+  const void* Q;
+  fa_strides xq;
+  void* O;
+  fa_strides xo;
+  float* L;
+  int group, max_q, wl, wr;
+  float scale;
+  Workspace ws;
+  uint8_t* workspace;
+  cudaStream_t stream;
+
+  fa::PartInfo* parts() const { return reinterpret_cast<fa::PartInfo*>(workspace); }
+  float* lpart() const { return reinterpret_cast<float*>(workspace + ws.l_at); }
+  float* opart() const { return reinterpret_cast<float*>(workspace + ws.o_at); }
+};
+
+// Tensor maps of the queries (column, head of a group, token, key head) and of the pages
+// (column, row, key head, page). `tokens`: of a query box.
+bool make_maps(const AttentionArgs& a, int tokens, CUtensorMap* q, CUtensorMap* k,
+               CUtensorMap* v) {
+  const fa_paged_cache& c = *a.c;
+  const int rows = c.page_size < fa::kKeyTile ? c.page_size : fa::kKeyTile;
+  return make_tmap(q, a.Q, c.dtype, {c.d, a.group, c.tokens, c.heads},
+                   {a.xq.h, a.xq.n, a.xq.h * a.group}, a.group, tokens) &&
+         make_tmap(k, c.k_pages, c.dtype, {c.d, c.page_size, c.heads, c.num_pages},
+                   {c.k_row, c.k_head, c.k_page}, rows, 1) &&
+         make_tmap(v, c.v_pages, c.dtype, {c.d, c.page_size, c.heads, c.num_pages},
+                   {c.v_row, c.v_head, c.v_page}, rows, 1);
+}
+
+// Joins the parts; launched so that it may begin while the kernel before it still runs
+// (it waits for that kernel's end before it reads anything).
+template <int D, int WPR, bool BF16>
+int launch_merge(const AttentionArgs& a) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kGrid, static_cast<unsigned>(a.ws.rows * WPR * 32 / fa::kMergeThreads));
+  cfg.blockDim = dim3(fa::kMergeThreads);
+  cfg.stream = a.stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, WPR, BF16>,
+                            static_cast<const float*>(a.opart()),
+                            static_cast<const float*>(a.lpart()),
+                            static_cast<const fa::PartInfo*>(a.parts()), kGrid, a.ws.rows, a.group,
+                            static_cast<uint16_t*>(a.O), strides(a.xo), a.L,
+                            a.c->tokens) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+// The least cost (in key tiles) that is worth a CTA of its own.
+constexpr int kStepLeast = 4;
+
+template <int D, int NQ, bool BF16>
+int launch_step(const AttentionArgs& a) {
+  using Lay = fa::StepLayout<D, NQ>;
+  static_assert(Lay::kBytes <= kMaxDynSmem, "shared memory");
+  auto kern = fa::fa_paged_step_kernel<D, NQ, BF16>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(Lay::kBytes)) != cudaSuccess)
+    return FA_ERR_CUDA;
+  CUtensorMap q, k, v;
+  if (!make_maps(a, a.max_q, &q, &k, &v)) return FA_ERR_CUDA;
+  kern<<<kGrid, Lay::kThreads, Lay::kBytes, a.stream>>>(
+      q, k, v, view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.opart(),
+      a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kStepLeast, a.scale * kLog2e);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return launch_merge<D, 8, BF16>(a);
+}
+
 template <int D, bool BF16>
-int launch_simple(const fa_paged_cache& c, const void* Q, const fa_strides& xq, void* O,
-                  const fa_strides& xo, float* L, int Hq, int max_q, int wl, int wr, float scale,
-                  cudaStream_t stream) {
+int launch_simple(const AttentionArgs& a) {
+  const fa_paged_cache& c = *a.c;
   const fa::PagedKv kv{static_cast<const uint16_t*>(c.k_pages),
                        static_cast<const uint16_t*>(c.v_pages),
                        {static_cast<long>(c.k_page), static_cast<long>(c.k_head),
                         static_cast<long>(c.k_row)},
                        {static_cast<long>(c.v_page), static_cast<long>(c.v_head),
                         static_cast<long>(c.v_row)}};
-  const dim3 grid(static_cast<unsigned>(c.tokens), static_cast<unsigned>(Hq));
-  fa::fa_paged_simple_kernel<D, BF16><<<grid, fa::kSimpleThreads, 0, stream>>>(
-      view_of(c), kv, static_cast<const uint16_t*>(Q), strides(xq), static_cast<uint16_t*>(O),
-      strides(xo), L, Hq, max_q, edge(wl), edge(wr), scale * kLog2e);
+  const dim3 grid(static_cast<unsigned>(c.tokens), static_cast<unsigned>(a.group * c.heads));
+  fa::fa_paged_simple_kernel<D, BF16><<<grid, fa::kSimpleThreads, 0, a.stream>>>(
+      view_of(c), kv, static_cast<const uint16_t*>(a.Q), strides(a.xq),
+      static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.group * c.heads, a.max_q, a.wl, a.wr,
+      a.scale * kLog2e);
   return launch_status();
+}
+
+template <int D, bool BF16>
+int launch_attention(const AttentionArgs& a) {
+  switch (a.ws.rows) {
+    case 16: return launch_step<D, 16, BF16>(a);
+    case 32: return launch_step<D, 32, BF16>(a);
+    case 64: return launch_step<D, 64, BF16>(a);
+    default: return launch_simple<D, BF16>(a);
+  }
 }
 
 }  // namespace
@@ -189,8 +345,10 @@ int fa_paged_append(const fa_paged_cache* cache, const void* K, const fa_strides
 }
 
 size_t fa_paged_workspace_size(int tokens, int max_q, int Hq, int heads, int d) {
-  if (tokens < 0 || max_q < 0 || Hq < 0 || heads <= 0 || d < 0) return static_cast<size_t>(-1);
-  return 0;
+  if (tokens < 0 || max_q < 0 || Hq < 0 || heads <= 0 || d < 0 || Hq % heads != 0)
+    return static_cast<size_t>(-1);
+  if (tokens == 0 || max_q == 0 || Hq == 0) return 0;
+  return workspace_for(max_q, Hq / heads, d).bytes;
 }
 
 int fa_paged_attention(const fa_paged_cache* cache, const void* Q, const fa_strides* xq, void* O,
@@ -202,23 +360,36 @@ int fa_paged_attention(const fa_paged_cache* cache, const void* Q, const fa_stri
   if (Hq < 0 || Hq % cache->heads != 0 || max_q < 0) return FA_ERR_INVALID;
   if (!(scale > 0.f) || !isfinite(scale)) return FA_ERR_INVALID;
   if (Hq / cache->heads > 128) return FA_ERR_UNSUPPORTED;
-  if (cache->batch == 0 || cache->tokens == 0 || Hq == 0) return FA_OK;
-  if (!ok_ptr(Q) || !ok_ptr(O) || !ok_ptr(L) || !ok_strides(xq) || !ok_strides(xo))
+  if (cache->batch == 0 || cache->tokens == 0 || Hq == 0 || max_q == 0) return FA_OK;
+  if (!ok_ptr(Q) || !ok_ptr(O) || !ok_ptr(L, 4) || !ok_strides(xq) || !ok_strides(xo))
     return FA_ERR_INVALID;
-  const size_t need =
-      fa_paged_workspace_size(cache->tokens, max_q, Hq, cache->heads, cache->d);
-  if (need > 0 && (!ok_ptr(workspace, 256) || workspace_bytes < need)) return FA_ERR_INVALID;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cache->num_pages == 0 || cache->table_width == 0) return FA_ERR_INVALID;
+  const int group = Hq / cache->heads;
+  if (!steps(xq->h, Hq) || !steps(xq->n, cache->tokens) || !steps(xo->h, Hq) ||
+      !steps(xo->n, cache->tokens) || !steps(cache->k_row, cache->page_size) ||
+      !steps(cache->k_head, cache->heads) || !steps(cache->k_page, cache->num_pages) ||
+      !steps(cache->v_row, cache->page_size) || !steps(cache->v_head, cache->heads) ||
+      !steps(cache->v_page, cache->num_pages))
+    return FA_ERR_UNSUPPORTED;
+  const Workspace ws = workspace_for(max_q, group, cache->d);
+  if (!ok_ptr(workspace, 256) || workspace_bytes < ws.bytes) return FA_ERR_INVALID;
+  const AttentionArgs a{cache,
+                        Q,
+                        *xq,
+                        O,
+                        *xo,
+                        L,
+                        group,
+                        max_q < cache->tokens ? max_q : cache->tokens,
+                        edge(window_left),
+                        edge(window_right),
+                        scale,
+                        ws,
+                        static_cast<uint8_t*>(workspace),
+                        static_cast<cudaStream_t>(stream)};
   const bool bf = cache->dtype == FA_BF16;
-  if (cache->d == 64)
-    return bf ? launch_simple<64, true>(*cache, Q, *xq, O, *xo, L, Hq, max_q, window_left,
-                                        window_right, scale, s)
-              : launch_simple<64, false>(*cache, Q, *xq, O, *xo, L, Hq, max_q, window_left,
-                                         window_right, scale, s);
-  return bf ? launch_simple<128, true>(*cache, Q, *xq, O, *xo, L, Hq, max_q, window_left,
-                                       window_right, scale, s)
-            : launch_simple<128, false>(*cache, Q, *xq, O, *xo, L, Hq, max_q, window_left,
-                                        window_right, scale, s);
+  if (cache->d == 64) return bf ? launch_attention<64, true>(a) : launch_attention<64, false>(a);
+  return bf ? launch_attention<128, true>(a) : launch_attention<128, false>(a);
 }
 
 int fa_paged_device_status(void* stream) {

@@ -40,6 +40,30 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedView& c, int b, int max_q
   return s;
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+  return x;
+}
+// Named barrier over `count` threads that tells each whether any of them passed true.
+__device__ __forceinline__ bool named_bar_or(int id, int count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+
 // The last b < batch with cu_q[b] <= t, or -1; called by a whole warp. Each round probes 32
 // places of what is left, so a batch of up to 1024 takes two dependent loads.
 __device__ __forceinline__ int owner_of(const int* cu_q, int batch, int t, int lane) {
@@ -56,5 +80,45 @@ __device__ __forceinline__ int owner_of(const int* cu_q, int batch, int t, int l
   }
   return lo;
 }
+
+// Pages of one sequence as a warp reads them ahead: lane i holds the indexes of pages
+// base + i and base + 32 + i, so the table is read one coalesced load at a time, a window
+// ahead of its use. Indexes outside the pool become num_pages, whose rows the tensor maps
+// read as zeros; *bad is set.
+struct PageWindow {
+  const int* row;  // the sequence's table row
+  int width, pages;
+  int base, now, then;
+  bool bad;
+
+  __device__ __forceinline__ int fetch(int i) {
+    if (i >= width) return pages;
+    const int p = row[i];
+    return p;
+  }
+  __device__ __forceinline__ void start(const PagedView& c, int b, int first, int lane) {
+    row = c.table + static_cast<long>(b) * c.table_row;
+    width = c.table_width;
+    pages = c.num_pages;
+    base = first;
+    now = fetch(base + lane);
+    then = fetch(base + 32 + lane);
+  }
+  // Page i of the sequence, for every lane its own i (ascending over calls; all lanes' i
+  // lie in one window).
+  __device__ __forceinline__ int get(int i, int first, int lane) {
+    while (first >= base + 32) {
+      base += 32;
+      now = then;
+      then = fetch(base + 32 + lane);
+    }
+    int p = __shfl_sync(0xffffffffu, now, (i - base) & 31);
+    if (static_cast<unsigned>(p) >= static_cast<unsigned>(pages)) {
+      p = pages;
+      bad = true;
+    }
+    return p;
+  }
+};
 
 }  // namespace fa

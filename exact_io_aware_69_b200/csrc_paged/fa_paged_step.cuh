@@ -1,0 +1,471 @@
+// fa_paged_step.cuh -- attention of a few new tokens per sequence over a paged cache: the
+// decode step and the check of drafted tokens (up to 64 rows per key head, a row being one
+// token's query head).
+//
+// The pass is bound by reading K and V from HBM once: with R rows it does 4 R d
+// operations per 4 d bytes of a key. So the work is laid out along the keys
+// (fa_paged_split.cuh: one persistent CTA per SM, each with the same number of key tiles),
+// a producer warp streams the pages' tiles through a ring without a pause across items,
+// and both products go to the tensor cores with the keys on the 128-row side, where a tile
+// of them fills an MMA whatever R is:
+//   S^T_j = K_j Q^T            M = 128 keys, N = NQ query columns, K = d
+//   O^T  += V_j^T P_j^T        M = d (128), N = NQ, K = 128 keys; A = V_j read M-major,
+//                              B = P_j^T from shared memory (NQ rows x 128 keys, 16-bit)
+// At d = 64 the second MMA keeps M = 128 (its A then reaches into the K tile behind V in
+// the stage): lanes 64-127 of O^T hold products nobody reads.
+//
+// Column q of an item is token q / group and query head q % group of its key head's group,
+// so all query heads that share a key head share one pass over it.
+//
+// Softmax: thread r of a warpgroup owns key r of the tile and 16 or 32 query columns. The
+// reference m of a column moves only when a score exceeds it by more than 2^8; whether
+// any does is one barrier-vote per tile, and only then are the tile's maxima exchanged and
+// O^T rescaled. Two sums per column: of the 16-bit weights, which normalises O, and of the
+// unrounded ones, which gives L.
+//
+// V rows of keys that no row of the item sees -- behind the sequence's end, before its
+// window, or in pages that are not loaded -- are zeroed in shared memory, since 0 times
+// whatever an unwritten row holds need not be 0.
+//
+// Warps: 4 (NQ <= 32) or 8 (NQ = 64) softmax warps, the TMA producer, the MMA issuer.
+#pragma once
+
+#include "fa_paged_split.cuh"
+
+namespace fa {
+
+constexpr float kStepRescaleSlack = 8.0f;
+
+template <int D, int NQ>
+struct StepLayout {
+  static constexpr int kGroups = NQ == 64 ? 2 : 1;  // softmax warpgroups
+  static constexpr int kCols = NQ / kGroups;        // query columns of a softmax thread
+  static constexpr int kSoftmax = 128 * kGroups;
+  static constexpr int kThreads = kSoftmax + 64;
+  static constexpr uint32_t kTileBytes = kKeyTile * D * 2;
+  static constexpr uint32_t kChunkBytes = kKeyTile * 128;  // 128 rows x 64 values
+  static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // V tile, then K tile
+  static constexpr int kStages = (D == 128 ? 3 : 6) - (NQ == 64 ? (D == 128 ? 1 : 2) : 0);
+  static constexpr uint32_t kQChunk = NQ * 128;  // NQ rows x 64 values
+  static constexpr uint32_t kQBytes = kQChunk * (D / 64);
+  static constexpr uint32_t kPBytes = NQ * 256;  // NQ rows x 128 keys
+  static constexpr uint32_t kQ = kStages * kStageBytes;   // 2 buffers
+  static constexpr uint32_t kP = kQ + 2 * kQBytes;        // 2 buffers
+  static constexpr uint32_t kRed = kP + 2 * kPBytes;      // [group][warp][column] maxima
+  static constexpr uint32_t kSums = kRed + 4 * NQ * 4;    // [group][warp][2][column]
+  static constexpr uint32_t kTok = kSums + 8 * NQ * 4;    // [column] token of a column
+  static constexpr uint32_t kBounds = kTok + NQ * 4;
+  static constexpr uint32_t kBar = kBounds + 32;
+  static constexpr int kNumBars = 2 * kStages + 10;
+  static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
+  static constexpr uint32_t kAbort = kTmemSlot + 8;
+  static constexpr uint32_t kBytes = kAbort + 8 + 1024;
+  // TMEM: S^T buffers at 0 and NQ, O^T at 2 NQ
+  static constexpr uint32_t tO = 2 * NQ;
+  static constexpr uint32_t kTmemCols = NQ == 16 ? 64 : NQ == 32 ? 128 : 256;
+  // barriers
+  static constexpr int bFull = 0, bEmpty = kStages, bQFull = 2 * kStages, bQEmpty = bQFull + 2,
+                       bSFull = bQEmpty + 2, bPFull = bSFull + 2,
+                       bDone = bPFull + 2;  // the product of a P buffer has landed
+};
+
+// Byte of (row, key) in an NQ-row, 128-byte-swizzled tile of 128 16-bit columns.
+template <int NQ>
+__device__ __forceinline__ uint32_t step_swz(int row, int col) {
+  const int byte = (col & 63) * 2;
+  return static_cast<uint32_t>((col >> 6) * NQ * 128 + row * 128 +
+                               ((((byte >> 4) ^ (row & 7)) << 4) | (byte & 15)));
+}
+
+template <int C>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t* r) {
+  if constexpr (C == 16) {
+    tmem_ld16(addr, r);
+    tmem_wait_ld();
+    reg_fence16(r);
+  } else {
+    tmem_ld32(addr, r);
+    tmem_wait_ld();
+    reg_fence32(r);
+  }
+}
+
+// Issues the loads of the pages of tile `tile` that hold keys of [keys.lo, keys.hi] into
+// `vdst` and `kdst`, by all lanes of a warp: up to 8 pages x (K, V) x 64-column chunks.
+// Returns the pages' count times a page's rows, known before any load is issued.
+struct TilePages {
+  int first, count;  // pages of the sequence
+  int rows;          // of a page in this tile
+  __device__ __forceinline__ TilePages(int tile, const KeyRange& keys, int shift) {
+    const int k0 = max(tile * kKeyTile, keys.lo), k1 = min(tile * kKeyTile + kKeyTile - 1, keys.hi);
+    first = k0 >> shift;
+    count = (k1 >> shift) - first + 1;
+    rows = min(1 << shift, kKeyTile);
+  }
+};
+template <int D>
+__device__ __forceinline__ void load_tile_pages(const TilePages& t, int tile, int shift,
+                                                PageWindow& win, const CUtensorMap* mapA,
+                                                uint32_t dstA, uint32_t barA,
+                                                const CUtensorMap* mapB, uint32_t dstB,
+                                                uint32_t barB, int head, int lane) {
+  constexpr int kChunks = D / 64;
+  const int per_page = (mapB != nullptr ? 2 : 1) * kChunks;
+  // lane -> (page, operand, chunk); 8 pages x 4 pieces at most, one per lane
+  const int i = lane / per_page;
+  const int piece = lane - i * per_page;
+  const int page = win.get(t.first + min(i, t.count - 1), t.first, lane);
+  if (i < t.count) {
+    const int key = max((t.first + i) << shift, tile * kKeyTile);  // first key of the box
+    const bool second = piece >= kChunks;
+    const int chunk = second ? piece - kChunks : piece;
+    const uint32_t at = static_cast<uint32_t>(chunk * kKeyTile + key - tile * kKeyTile) * 128u;
+    tma_load_4d((second ? dstB : dstA) + at, second ? mapB : mapA, chunk * 64,
+                key & ((1 << shift) - 1), head, page, second ? barB : barA);
+  }
+}
+
+template <int D, int NQ, bool BF16>
+__global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
+    fa_paged_step_kernel(const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const PagedView c,
+                         uint16_t* __restrict__ O, Strides so, float* __restrict__ L,
+                         float* __restrict__ Opart, float* __restrict__ Lpart,
+                         PartInfo* __restrict__ parts, int group, int max_q, int wl, int wr,
+                         int least, float scale_log2) {
+  using Lay = StepLayout<D, NQ>;
+  constexpr int S = Lay::kStages;
+  constexpr int C = Lay::kCols;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t pad = ((raw_base + 1023u) & ~1023u) - raw_base;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sbase = raw_base + pad;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return sbase + Lay::kBar + 8u * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbort);
+  int* tok = reinterpret_cast<int*>(smem + Lay::kTok);
+  Bound* bounds = reinterpret_cast<Bound*>(smem + Lay::kBounds);
+  constexpr int kProducer = Lay::kSoftmax / 32, kMma = kProducer + 1;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bar(Lay::bFull + s), 1);
+      mbar_init(bar(Lay::bEmpty + s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(Lay::bQFull + b), 1);
+      mbar_init(bar(Lay::bQEmpty + b), 1);
+      mbar_init(bar(Lay::bSFull + b), 1);
+      mbar_init(bar(Lay::bPFull + b), Lay::kSoftmax);
+      mbar_init(bar(Lay::bDone + b), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(sbase + Lay::kTmemSlot, Lay::kTmemCols);
+    tmem_relinquish();
+  }
+  // columns no query fills: zeros, so that their scores are 0 and move nothing
+  for (uint32_t i = threadIdx.x; i < 2 * Lay::kQBytes / 16; i += Lay::kThreads)
+    *reinterpret_cast<uint4*>(smem + Lay::kQ + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  if (threadIdx.x < NQ) tok[threadIdx.x] = threadIdx.x / group;
+  tc_fence_before();
+  split_bounds<true>(c, max_q, max_q, wl, wr, least, reinterpret_cast<long long*>(smem), bounds);
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Lay::kTmemSlot);
+  Walk w(c, max_q, max_q, wl, wr, bounds);
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      tma_prefetch(&tmQ);
+      tma_prefetch(&tmK);
+      tma_prefetch(&tmV);
+      write_part_info(c, max_q, max_q, bounds, parts);
+    }
+    __syncwarp();
+    const uint32_t q_bytes = static_cast<uint32_t>(group) * max_q * D * 2;
+    int it = 0, item = 0;
+    bool ok = true;
+    PageWindow win;
+    win.bad = false;
+    for (; w.more && ok; w.next(c, max_q, max_q, wl, wr)) {
+      if (w.j0 >= w.j1) continue;
+      const int qb = item & 1;
+      ok = item < 2 || mbar_wait(bar(Lay::bQEmpty + qb), static_cast<uint32_t>(item / 2 - 1) & 1,
+                                 abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      win.start(c, w.at.b, (w.keys.first + w.j0) * kKeyTile >> c.page_shift, lane);
+      if (lane == 0) {
+        mbar_expect_tx(bar(Lay::bQFull + qb), q_bytes);
+        for (int i = 0; i < D / 64; ++i)
+          tma_load_4d(sbase + Lay::kQ + qb * Lay::kQBytes + i * Lay::kQChunk, &tmQ, i * 64, 0,
+                      w.seq.begin, w.at.h, bar(Lay::bQFull + qb));
+      }
+      ++item;
+      for (int j = w.j0; j < w.j1; ++j, ++it) {
+        const int st = it % S;
+        const int tile = w.keys.first + j;
+        const TilePages pages(tile, w.keys, c.page_shift);
+        ok = it < S || mbar_wait(bar(Lay::bEmpty + st), static_cast<uint32_t>(it / S - 1) & 1,
+                                 abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = sbase + st * Lay::kStageBytes;
+        if (lane == 0)
+          mbar_expect_tx(bar(Lay::bFull + st),
+                         static_cast<uint32_t>(pages.count * pages.rows) * D * 4);
+        __syncwarp();
+        load_tile_pages<D>(pages, tile, c.page_shift, win, &tmV, dst, bar(Lay::bFull + st), &tmK,
+                           dst + Lay::kTileBytes, bar(Lay::bFull + st), w.at.h, lane);
+      }
+    }
+    if (win.bad) atomicExch(&g_fa_status, kStatusInvalid);
+  } else if (warp == kMma) {
+    // -------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_f16_f32(kKeyTile, NQ, BF16, false, false);
+      constexpr uint32_t id_o = idesc_f16_f32(128, NQ, BF16, true, false);
+      bool ok = true;
+      // O^T += V^T P^T of tile t of the CTA's tiles (accumulate: not an item's first)
+      auto product = [&](int t, bool accumulate) -> bool {
+        const int st = t % S, pb = t & 1;
+        if (!mbar_wait(bar(Lay::bPFull + pb), static_cast<uint32_t>(t >> 1) & 1, abort_flag))
+          return false;
+        tc_fence_after();
+        const uint64_t dv = sdesc_sw128(sbase + st * Lay::kStageBytes, Lay::kChunkBytes, 1024);
+        const uint64_t dp = sdesc_sw128(sbase + Lay::kP + pb * Lay::kPBytes, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < kKeyTile / 16; ++k)
+          mma_ss(tmem + Lay::tO, sdesc_advance(dv, k * 2048),
+                 sdesc_advance(dp, (k >> 2) * Lay::kQChunk + (k & 3) * 32), id_o,
+                 (accumulate || k > 0) ? 1u : 0u);
+        mma_commit(bar(Lay::bEmpty + st));
+        mma_commit(bar(Lay::bDone + pb));
+        return true;
+      };
+      int it = 0, item = 0;
+      bool last_accumulates = false;
+      for (; w.more && ok; w.next(c, max_q, max_q, wl, wr)) {
+        if (w.j0 >= w.j1) continue;
+        const int qb = item & 1;
+        ok = mbar_wait(bar(Lay::bQFull + qb), static_cast<uint32_t>(item >> 1) & 1, abort_flag);
+        const uint64_t dq = sdesc_sw128(sbase + Lay::kQ + qb * Lay::kQBytes, 16, 1024);
+        for (int j = w.j0; ok && j < w.j1; ++j, ++it) {
+          const int st = it % S;
+          ok = mbar_wait(bar(Lay::bFull + st), static_cast<uint32_t>(it / S) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dk =
+              sdesc_sw128(sbase + st * Lay::kStageBytes + Lay::kTileBytes, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + (it & 1) * NQ,
+                   sdesc_advance(dk, (k >> 2) * Lay::kChunkBytes + (k & 3) * 32),
+                   sdesc_advance(dq, (k >> 2) * Lay::kQChunk + (k & 3) * 32), id_s,
+                   k > 0 ? 1u : 0u);
+          mma_commit(bar(Lay::bSFull + (it & 1)));
+          if (j == w.j1 - 1) mma_commit(bar(Lay::bQEmpty + qb));
+          if (it > 0) ok = product(it - 1, last_accumulates);
+          last_accumulates = j > w.j0;
+        }
+        ++item;
+      }
+      if (ok && it > 0) product(it - 1, last_accumulates);
+    }
+  } else {
+    // ----------------------------------------------------------------- softmax
+    const int wg = warp >> 2;           // columns wg * C .. wg * C + C - 1
+    const int r = threadIdx.x & 127;    // key of the tile = TMEM lane
+    const int q0 = wg * C;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float* red = reinterpret_cast<float*>(smem + Lay::kRed) + wg * 4 * C;
+    float* sums = reinterpret_cast<float*>(smem + Lay::kSums) + wg * 8 * C;
+    const int gbar = 1 + wg;
+    bool ok = true;
+    int it = 0;
+    for (; w.more && ok; w.next(c, max_q, max_q, wl, wr)) {
+      const int rows = w.seq.n * group;
+      const int off = w.seq.nk - w.seq.n;
+      // keys that every row sees
+      const int all_lo = w.seq.n - 1 + off - wl, all_hi = min(w.seq.nk - 1, off + wr);
+      float m[C], l[C], l_o[C];
+#pragma unroll
+      for (int q = 0; q < C; ++q) {
+        m[q] = -INFINITY;
+        l[q] = 0.f;  // this thread's (key's) share of the sums
+        l_o[q] = 0.f;
+      }
+      for (int j = w.j0; j < w.j1; ++j, ++it) {
+        const int b = it & 1;
+        const int key0 = (w.keys.first + j) * kKeyTile;
+        const int key = key0 + r;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bSFull + b),
+                                               static_cast<uint32_t>(it >> 1) & 1, abort_flag));
+        float s[C];
+        bool raise = !ok;
+        if (ok) {
+          tc_fence_after();
+          uint32_t sr[C];
+          tmem_ld_cols<C>(lane_base + b * NQ + q0, sr);
+#pragma unroll
+          for (int q = 0; q < C; ++q) s[q] = __uint_as_float(sr[q]) * scale_log2;
+          if (key0 < all_lo || key0 + kKeyTile - 1 > all_hi) {  // an edge of the mask
+#pragma unroll
+            for (int q = 0; q < C; ++q) {
+              const int mid = tok[q0 + q] + off;
+              if (key > min(w.seq.nk - 1, mid + wr) || key < mid - wl) s[q] = -INFINITY;
+            }
+            if (wg == 0 && (key < w.keys.lo || key > w.keys.hi)) {
+              const uint32_t v = sbase + (it % S) * Lay::kStageBytes + r * 128;
+              // the stage has landed: its K has been multiplied
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 v + (i >> 3) * Lay::kChunkBytes + (i & 7) * 16),
+                             "r"(0)
+                             : "memory");
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < C; ++q) raise = raise || s[q] > m[q] + kStepRescaleSlack;
+        }
+        if (named_bar_or(gbar, 128, raise)) {
+          ok = named_bar_and(gbar, 128, ok);
+          if (!ok) break;
+#pragma unroll
+          for (int q = 0; q < C; ++q) {
+            const float mw = warp_max(s[q]);
+            if (lane == 0) red[(warp & 3) * C + q] = mw;
+          }
+          named_bar_sync(gbar, 128);
+          float alpha[C];
+#pragma unroll
+          for (int q = 0; q < C; ++q) {
+            const float top =
+                fmaxf(fmaxf(red[q], red[C + q]), fmaxf(red[2 * C + q], red[3 * C + q]));
+            const float m_new = top > m[q] + kStepRescaleSlack ? top : m[q];
+            alpha[q] = m_new == -INFINITY ? 1.f : ex2_approx(m[q] - m_new);  // 0 at first
+            m[q] = m_new;
+            l[q] *= alpha[q];
+            l_o[q] *= alpha[q];
+          }
+          if (j > w.j0) {  // O^T holds products: rescale it once the last one has landed
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(bar(Lay::bDone + (b ^ 1)),
+                                      static_cast<uint32_t>((it - 1) >> 1) & 1, abort_flag));
+            if (ok) {
+              tc_fence_after();
+              uint32_t o[C];
+              tmem_ld_cols<C>(lane_base + Lay::tO + q0, o);
+#pragma unroll
+              for (int q = 0; q < C; ++q)
+                o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha[q]);
+              if constexpr (C == 16)
+                tmem_st16(lane_base + Lay::tO + q0, o);
+              else
+                tmem_st32(lane_base + Lay::tO + q0, o);
+              tmem_wait_st();
+            }
+          }
+        }
+        // P_j^T into buffer b, once the product before last has read it
+        if (ok && it >= 2)
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(bar(Lay::bDone + b),
+                                    static_cast<uint32_t>((it - 2) >> 1) & 1, abort_flag));
+        uint8_t* pt = smem + Lay::kP + b * Lay::kPBytes;
+#pragma unroll
+        for (int q = 0; q < C; ++q) {
+          // a column that has seen no key yet has m = -inf and gets 0
+          const float p = m[q] == -INFINITY ? 0.f : ex2_approx(s[q] - m[q]);
+          const uint32_t pk = pack2<BF16>(p, 0.f);
+          float pr, unused;
+          unpack2<BF16>(pk, pr, unused);
+          l[q] += p;
+          l_o[q] += pr;
+          *reinterpret_cast<uint16_t*>(pt + step_swz<NQ>(q0 + q, r)) =
+              static_cast<uint16_t>(pk & 0xFFFFu);
+        }
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar(Lay::bPFull + b));
+        // a wait that gave up in one warp reaches the others at the next vote
+      }
+      // the item's last product, and the sums over the tile's 128 keys
+      const bool some = w.j1 > w.j0;
+      ok = __all_sync(0xffffffffu,
+                      ok && (!some || mbar_wait(bar(Lay::bDone + ((it - 1) & 1)),
+                                                static_cast<uint32_t>((it - 1) >> 1) & 1,
+                                                abort_flag)));
+#pragma unroll
+      for (int q = 0; q < C; ++q) {
+        if (q0 + q < rows) {
+          const float a = warp_sum(l[q]), e = warp_sum(l_o[q]);
+          if (lane == 0) {
+            sums[((warp & 3) * 2 + 0) * C + q] = a;
+            sums[((warp & 3) * 2 + 1) * C + q] = e;
+          }
+        }
+      }
+      ok = named_bar_and(gbar, 128, ok);
+      if (!ok) break;
+      uint32_t o[C];
+      if (some) {
+        tc_fence_after();
+        tmem_ld_cols<C>(lane_base + Lay::tO + q0, o);
+        tc_fence_before();
+      } else {
+#pragma unroll
+        for (int q = 0; q < C; ++q) o[q] = 0u;
+      }
+      const bool whole = w.j0 == 0 && w.j1 == w.keys.count;
+      const long slot = w.j0 > 0 ? 2L * blockIdx.x : 2L * blockIdx.x + 1;
+#pragma unroll
+      for (int q = 0; q < C; ++q) {
+        if (q0 + q < rows) {
+          float a = 0.f, e = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a += sums[(i * 2 + 0) * C + q];
+            e += sums[(i * 2 + 1) * C + q];
+          }
+          const float val = e > 0.f ? __uint_as_float(o[q]) / e : 0.f;  // no key: O = 0
+          const float L2 = a > 0.f ? m[q] + log2f(a) : -INFINITY;
+          if (whole) {
+            const int t = tok[q0 + q];
+            const int head = w.at.h * group + q0 + q - t * group;
+            const long row = w.seq.begin + t;
+            if (r < D)
+              O[row * so.sn + head * so.sh + r] =
+                  static_cast<uint16_t>(pack2<BF16>(val, 0.f) & 0xFFFFu);
+            if (r == 0)
+              L[static_cast<long>(head) * c.tokens + row] = L2 * 0.69314718055994530942f;
+          } else {
+            const long row = slot * NQ + q0 + q;
+            if (r < D) Opart[row * D + r] = val;
+            if (r == 0) Lpart[row] = L2;
+          }
+        }
+      }
+      named_bar_sync(gbar, 128);  // the sums are read before the next item's are written
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, Lay::kTmemCols);
+  }
+}
+
+}  // namespace fa

@@ -228,8 +228,11 @@ def test_bad_pages_and_lengths():
                                   batch.cu_q, seq_k, max_q=n, out=out)
         assert fa.device_status() == fa.FA_ERR_INVALID
         assert (o[n:2 * n] == 7).all()
-        want, _ = fa.paged_attention(batch.q, *batch.cache, max_q=n)
-        assert torch.equal(o[:n], want[:n]) and torch.equal(o[2 * n:], want[2 * n:])
+        # the split of the others' keys depends on the whole batch, and so do their roundings:
+        # held to the definition, with the left-out rows from a call that serves them
+        want, wantL = fa.paged_attention(batch.q, *batch.cache, max_q=n)
+        o[n:2 * n], L[:, n:2 * n] = want[n:2 * n], wantL[:, n:2 * n]
+        check(batch, o, L, 128 ** -0.5, CAUSAL)
         k, v = (torch.ones(3 * n, 2, 128, device="cuda").bfloat16() for _ in range(2))
         before = batch.k_pages.clone()
         table = batch.page_table.clone()
