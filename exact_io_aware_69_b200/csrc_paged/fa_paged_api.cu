@@ -9,8 +9,8 @@
 
 #include "fa_paged.h"
 #include "fa_paged_common.cuh"
+#include "fa_paged_chunk.cuh"
 #include "fa_paged_merge.cuh"
-#include "fa_paged_simple.cuh"
 #include "fa_paged_step.cuh"
 #include "fa_rope.cuh"
 
@@ -83,7 +83,7 @@ int check_cache(const fa_paged_cache* c, bool attention) {
     return FA_ERR_UNSUPPORTED;
   if (attention ? c->d != 64 && c->d != 128 : c->d % 16 != 0 || c->d > fa::kRopeMaxDim)
     return FA_ERR_UNSUPPORTED;
-  if (c->batch > 16384 || c->heads > 1024 || c->tokens > (1 << 28) ||
+  if (c->batch > 8192 || c->heads > 1024 || c->tokens > (1 << 28) ||
       static_cast<long long>(c->table_width) * c->page_size > (1 << 28))
     return FA_ERR_UNSUPPORTED;
   if (c->batch == 0 || c->tokens == 0) return FA_OK;
@@ -247,21 +247,29 @@ int launch_step(const AttentionArgs& a) {
   return launch_merge<D, 8, BF16>(a);
 }
 
+// ... and for chunks, whose tiles take longer and whose parts are larger.
+constexpr int kChunkLeast = 4;
+
 template <int D, bool BF16>
-int launch_simple(const AttentionArgs& a) {
-  const fa_paged_cache& c = *a.c;
-  const fa::PagedKv kv{static_cast<const uint16_t*>(c.k_pages),
-                       static_cast<const uint16_t*>(c.v_pages),
-                       {static_cast<long>(c.k_page), static_cast<long>(c.k_head),
-                        static_cast<long>(c.k_row)},
-                       {static_cast<long>(c.v_page), static_cast<long>(c.v_head),
-                        static_cast<long>(c.v_row)}};
-  const dim3 grid(static_cast<unsigned>(c.tokens), static_cast<unsigned>(a.group * c.heads));
-  fa::fa_paged_simple_kernel<D, BF16><<<grid, fa::kSimpleThreads, 0, a.stream>>>(
-      view_of(c), kv, static_cast<const uint16_t*>(a.Q), strides(a.xq),
-      static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.group * c.heads, a.max_q, a.wl, a.wr,
-      a.scale * kLog2e);
-  return launch_status();
+int launch_chunk(const AttentionArgs& a) {
+  using Lay = fa::ChunkLayout<D>;
+  static_assert(Lay::kSmem <= kMaxDynSmem, "shared memory");
+  auto kern = fa::fa_paged_chunk_kernel<D, BF16>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(Lay::kSmem)) != cudaSuccess)
+    return FA_ERR_CUDA;
+  // The kernel moves registers between warpgroups (setmaxnreg); its split adds up to
+  // exactly 168 registers per thread at launch (the build fails otherwise too).
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return FA_ERR_CUDA;
+  if (attr.numRegs != fa::kChunkLaunchRegs) return FA_ERR_UNSUPPORTED;
+  CUtensorMap q, k, v;
+  if (!make_maps(a, fa::kKeyTile / a.group, &q, &k, &v)) return FA_ERR_CUDA;
+  kern<<<kGrid, fa::kChunkThreads, Lay::kSmem, a.stream>>>(
+      q, k, v, view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.opart(),
+      a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kChunkLeast, a.scale * kLog2e);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return launch_merge<D, 1, BF16>(a);
 }
 
 template <int D, bool BF16>
@@ -270,7 +278,7 @@ int launch_attention(const AttentionArgs& a) {
     case 16: return launch_step<D, 16, BF16>(a);
     case 32: return launch_step<D, 32, BF16>(a);
     case 64: return launch_step<D, 64, BF16>(a);
-    default: return launch_simple<D, BF16>(a);
+    default: return launch_chunk<D, BF16>(a);
   }
 }
 

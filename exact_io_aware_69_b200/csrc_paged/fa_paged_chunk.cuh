@@ -1,0 +1,558 @@
+// fa_paged_chunk.cuh -- attention of longer chunks of new tokens over a paged cache.
+//
+// The pass is bound by the tensor cores and the exponentials: R query rows do 4 R d
+// operations per key, so every K and V tile brought on chip serves as many rows as tensor
+// memory holds, 2 x 128. Query rows are packed: row r of a 128-row tile is token
+// r / group and query head r % group of one key head's group, so that heads which share
+// keys share their tiles too, and a causal chunk's masked corner stays small (256 rows are
+// 256 / group tokens). When the group does not divide 128 the last rows of a tile are
+// zeros.
+//
+// Work is shared out along the keys (fa_paged_split.cuh): one persistent CTA per SM, all
+// with the same number of key tiles, whatever the mix of long chunks and single tokens; a
+// chunk's heavy last rows, or a long context behind a short chunk, cannot leave SMs idle.
+//
+// Warp roles (384 threads; at launch every thread may hold 168 registers, then warpgroup 2
+// hands registers to warpgroups 0 and 1):
+//   warps 0-3, 4-7  softmax of query tile 0 and 1: thread r owns row r (TMEM lane r) and
+//                   the tile's 128 scores of it, so its maximum needs no exchange.
+//   warp 8          K producer: the item's two Q tiles, then K tiles into 3 stages.
+//   warp 10         V producer, 2 stages. Both walk the page table by themselves, a window
+//                   of pages ahead, one box per page and 64 columns.
+//   warp 9          MMA issuer, in the order S0_j S1_j | PV0_j S0_j+1 PV1_j S1_j+1 | ...,
+//                   so that one warpgroup exponentiates while the tensor core multiplies
+//                   for the other. The order runs on across items: the next item's first
+//                   scores are computed while this one's outputs are stored.
+//
+// TMEM (512 columns at d = 128): S and P of warpgroup g at 128 g, O of g at 256 + d g. MMAs
+// of one thread run in order, so S_g,j+1 complete implies P_g,j V_j complete and O_g may be
+// rescaled without a further wait; the reference of a row moves only past 2^8.
+//
+// Scores are in base 2. Two row sums: of the 16-bit weights that the product multiplies
+// (normalises O) and of the unrounded ones (gives L). V rows of keys that no row of the
+// item sees are zeroed in shared memory before they are multiplied by weights of 0.
+#pragma once
+
+#include <type_traits>
+
+#include "fa_paged_step.cuh"
+
+namespace fa {
+
+constexpr int kChunkThreads = 384;
+constexpr int kChunkKWarp = 8, kChunkMmaWarp = 9, kChunkVWarp = 10;
+// 168 registers per thread at launch (the most 384 threads can have), then per
+// sub-partition 2 x 216 (softmax) + 72 (producers, MMA) = 3 x 168.
+constexpr int kChunkLaunchRegs = 168;
+constexpr int kChunkSoftmaxRegs = 216;
+constexpr int kChunkSmallRegs = 72;
+static_assert(2 * kChunkSoftmaxRegs + kChunkSmallRegs == 3 * kChunkLaunchRegs, "register split");
+constexpr float kChunkRescaleSlack = 8.0f;
+constexpr int kChunkRows = 256;  // rows of an item
+constexpr int kChunkKStages = 3;
+constexpr int kChunkVStages = 2;
+
+template <int D>
+struct ChunkLayout {
+  static constexpr uint32_t kTileBytes = kKeyTile * D * 2;
+  static constexpr uint32_t kChunkBytes = kKeyTile * 128;  // 128 rows x 64 values
+  static constexpr uint32_t kQ = 0;                        // 2 tiles
+  static constexpr uint32_t kK = kQ + 2 * kTileBytes;
+  static constexpr uint32_t kV = kK + kChunkKStages * kTileBytes;
+  static constexpr uint32_t kBounds = kV + kChunkVStages * kTileBytes;
+  static constexpr uint32_t kBar = kBounds + 32;
+  static constexpr int bQFull = 0, bQEmpty = 1, bKFull = 2, bKEmpty = bKFull + kChunkKStages,
+                       bVFull = bKEmpty + kChunkKStages, bVEmpty = bVFull + kChunkVStages,
+                       bSFull = bVEmpty + kChunkVStages, bPFull = bSFull + 2,
+                       bPHalf = bPFull + 2, bODone = bPHalf + 2, kNumBars = bODone + 2;
+  static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
+  static constexpr uint32_t kAbort = kTmemSlot + 8;
+  static constexpr uint32_t kBytes = kAbort + 8 + 1024;
+  // at least 120 KB, so that one CTA and its 512 TMEM columns sit on each SM; and the
+  // split's scratch (8 bytes per sequence) fits before the bounds
+  static constexpr uint32_t kSmem = kBytes > 136 * 1024 ? kBytes : 136 * 1024;
+  static constexpr uint32_t tS = 0;    // + 128 * warpgroup
+  static constexpr uint32_t tO = 256;  // + D * warpgroup
+};
+
+// The key tiles that each query tile of an item takes part in, within the CTA's part.
+struct ChunkTiles {
+  int lo[2], hi[2];  // [lo, hi); lo >= hi: none
+  int first, last;   // the union, [first, last)
+
+  __device__ __forceinline__ ChunkTiles(const Walk& w, int tpt, int wl, int wr) {
+    first = w.keys.first + w.j0;
+    last = w.keys.first + w.j1;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int p = 2 * w.at.p + g;
+      const KeyRange r = p * tpt < w.seq.n ? item_keys(p, tpt, w.seq.n, w.seq.nk, wl, wr)
+                                           : KeyRange{0, -1, 0, 0};
+      lo[g] = max(first, r.first);
+      hi[g] = min(last, r.first + r.count);
+    }
+  }
+  __device__ __forceinline__ bool in(int g, int tile) const {
+    return g ? tile >= lo[1] && tile < hi[1] : tile >= lo[0] && tile < hi[0];
+  }
+  __device__ __forceinline__ int count(int g) const {
+    return max(0, g ? hi[1] - lo[1] : hi[0] - lo[0]);
+  }
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    fa_paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
+                          const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const PagedView c,
+                          uint16_t* __restrict__ O, Strides so, float* __restrict__ L,
+                          float* __restrict__ Opart, float* __restrict__ Lpart,
+                          PartInfo* __restrict__ parts, int group, int max_q, int wl, int wr,
+                          int least,
+                          float scale_log2) {
+  using Lay = ChunkLayout<D>;
+  // Of every 16 exponential pairs, two go to the FMA pipe at d = 128, none at d = 64, and
+  // at d = 64 P V is issued in two halves: measured on the contiguous forward, whose inner
+  // loop this is.
+  constexpr int kPolyPairs = D == 64 ? 0 : 2;
+  constexpr int kPolyStride = kPolyPairs > 0 ? 16 / kPolyPairs : 16;
+  constexpr bool kSplitPV = D == 64;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t pad = ((raw_base + 1023u) & ~1023u) - raw_base;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sbase = raw_base + pad;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int tpt = kKeyTile / group;  // tokens of a query tile
+  const int tpi = 2 * tpt;           // tokens of an item
+  auto bar = [&](int i) -> uint32_t { return sbase + Lay::kBar + 8u * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbort);
+  Bound* bounds = reinterpret_cast<Bound*>(smem + Lay::kBounds);
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    mbar_init(bar(Lay::bQFull), 1);
+    mbar_init(bar(Lay::bQEmpty), 1);
+    for (int s = 0; s < kChunkKStages; ++s) {
+      mbar_init(bar(Lay::bKFull + s), 1);
+      mbar_init(bar(Lay::bKEmpty + s), 1);
+    }
+    for (int s = 0; s < kChunkVStages; ++s) {
+      mbar_init(bar(Lay::bVFull + s), 1);
+      mbar_init(bar(Lay::bVEmpty + s), 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(bar(Lay::bSFull + g), 1);
+      mbar_init(bar(Lay::bPFull + g), 128);
+      mbar_init(bar(Lay::bPHalf + g), 128);
+      mbar_init(bar(Lay::bODone + g), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kChunkMmaWarp) {
+    tmem_alloc(sbase + Lay::kTmemSlot, 512);
+    tmem_relinquish();
+  }
+  // scratch of the split lies behind the Q tiles, whose rows no box fills stay zero
+  for (uint32_t i = threadIdx.x; i < 2 * Lay::kTileBytes / 16; i += kChunkThreads)
+    *reinterpret_cast<uint4*>(smem + Lay::kQ + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  tc_fence_before();
+  split_bounds<false>(c, tpi, max_q, wl, wr, least,
+                      reinterpret_cast<long long*>(smem + Lay::kK), bounds);
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Lay::kTmemSlot);
+
+  if (warp >= 8) setmaxnreg_dec<kChunkSmallRegs>();  // every warp of warpgroup 2
+  if (warp == kChunkKWarp || warp == kChunkVWarp) {
+    // ---------------------------------------------------------------- producers
+    const bool is_k = warp == kChunkKWarp;
+    const CUtensorMap* map = is_k ? &tmK : &tmV;
+    const int stages = is_k ? kChunkKStages : kChunkVStages;
+    const uint32_t ring = sbase + (is_k ? Lay::kK : Lay::kV);
+    const int full = is_k ? Lay::bKFull : Lay::bVFull, empty = is_k ? Lay::bKEmpty : Lay::bVEmpty;
+    if (lane == 0) {
+      tma_prefetch(map);
+      if (is_k) tma_prefetch(&tmQ);
+    }
+    __syncwarp();
+    int st = 0, item = 0;
+    uint32_t phase = 1;  // of the stage's empty barrier: the first pass finds it free
+    bool ok = true;
+    PageWindow win;
+    win.bad = false;
+    for (Walk w(c, tpi, max_q, wl, wr, bounds); w.more && ok;
+         w.next(c, tpi, max_q, wl, wr)) {
+      if (w.j0 >= w.j1) continue;
+      const int first = w.keys.first + w.j0;
+      win.start(c, w.at.b, first * kKeyTile >> c.page_shift, lane);
+      if (is_k) {
+        ok = item == 0 ||
+             mbar_wait(bar(Lay::bQEmpty), static_cast<uint32_t>(item - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const ChunkTiles t(w, tpt, wl, wr);
+          const uint32_t bytes = static_cast<uint32_t>(tpt) * group * D * 2;
+          mbar_expect_tx(bar(Lay::bQFull), ((t.count(0) > 0) + (t.count(1) > 0)) * bytes);
+          for (int g = 0; g < 2; ++g)
+            if (t.count(g) > 0)
+              for (int i = 0; i < D / 64; ++i)
+                tma_load_4d(sbase + Lay::kQ + g * Lay::kTileBytes + i * Lay::kChunkBytes, &tmQ,
+                            i * 64, 0, w.seq.begin + (2 * w.at.p + g) * tpt, w.at.h,
+                            bar(Lay::bQFull));
+        }
+        __syncwarp();
+        ++item;
+      }
+      for (int tile = first; tile < w.keys.first + w.j1; ++tile) {
+        const TilePages pages(tile, w.keys, c.page_shift);
+        ok = mbar_wait(bar(empty + st), phase, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0)
+          mbar_expect_tx(bar(full + st),
+                         static_cast<uint32_t>(pages.count * pages.rows) * D * 2);
+        __syncwarp();
+        load_tile_pages<D>(pages, tile, c.page_shift, win, map, ring + st * Lay::kTileBytes,
+                           bar(full + st), nullptr, 0, 0, w.at.h, lane);
+        if (++st == stages) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (win.bad) atomicExch(&g_fa_status, kStatusInvalid);
+    if (is_k && lane == 0) write_part_info(c, tpi, max_q, bounds, parts);
+  } else if (warp == kChunkMmaWarp) {
+    // -------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_f16_f32(kKeyTile, kKeyTile, BF16, false, false);
+      constexpr uint32_t idesc_o = idesc_f16_f32(kKeyTile, D, BF16, false, true);
+      bool ok = true;
+      int ks = 0, vs = 0, item = 0;
+      uint32_t kphase = 0, vphase = 0;
+      uint32_t pphase[2] = {0, 0};
+      // the product that query tile g still owes for the previous tile: 0 none, 1 an
+      // item's first (O is overwritten), 2 a later one; + 4: the item's last
+      int owed[2] = {0, 0};
+      auto product = [&](int g, bool wait_v) -> bool {
+        if (!mbar_wait(bar((kSplitPV ? Lay::bPHalf : Lay::bPFull) + g), pphase[g], abort_flag))
+          return false;
+        if (wait_v && !mbar_wait(bar(Lay::bVFull + vs), vphase, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t dv =
+            sdesc_sw128(sbase + Lay::kV + vs * Lay::kTileBytes, Lay::kChunkBytes, 1024);
+        const uint32_t a_p = tmem + Lay::tS + g * 128;  // P packed in 64 columns
+        const uint32_t d_o = tmem + Lay::tO + g * D;
+        const bool accumulate = (owed[g] & 3) == 2;
+#pragma unroll
+        for (int k = 0; k < kKeyTile / 32; ++k)
+          mma_ts(d_o, a_p + k * 8, sdesc_step(dv, k * 2048), idesc_o,
+                 (accumulate || k > 0) ? 1u : 0u);
+        if (kSplitPV) {
+          if (!mbar_wait(bar(Lay::bPFull + g), pphase[g], abort_flag)) return false;
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int k = kKeyTile / 32; k < kKeyTile / 16; ++k)
+          mma_ts(d_o, a_p + k * 8, sdesc_step(dv, k * 2048), idesc_o, 1u);
+        pphase[g] ^= 1;
+        if (owed[g] & 4) mma_commit(bar(Lay::bODone + g));
+        owed[g] = 0;
+        return true;
+      };
+      bool v_owed = false;  // the previous tile's V stage is to be released
+      for (Walk w(c, tpi, max_q, wl, wr, bounds); w.more && ok;
+           w.next(c, tpi, max_q, wl, wr)) {
+        if (w.j0 >= w.j1) continue;
+        const ChunkTiles t(w, tpt, wl, wr);
+        bool q_waited = false;
+        for (int tile = t.first; ok && tile < t.last; ++tile) {
+          bool v_waited = false, k_waited = false;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (ok && owed[g]) {
+              ok = product(g, !v_waited);
+              v_waited = true;
+            }
+            if (ok && t.in(g, tile)) {
+              if (!q_waited) {
+                ok = mbar_wait(bar(Lay::bQFull), static_cast<uint32_t>(item) & 1, abort_flag);
+                q_waited = true;
+              }
+              if (ok && !k_waited) {
+                ok = mbar_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
+                k_waited = true;
+              }
+              if (ok) {
+                tc_fence_after();
+                const uint64_t dq = sdesc_sw128(sbase + Lay::kQ + g * Lay::kTileBytes, 16, 1024);
+                const uint64_t dk = sdesc_sw128(sbase + Lay::kK + ks * Lay::kTileBytes, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                  const uint32_t koff = (k >> 2) * Lay::kChunkBytes + (k & 3) * 32;
+                  mma_ss(tmem + Lay::tS + g * 128, sdesc_step(dq, koff), sdesc_step(dk, koff),
+                         idesc_s, k > 0 ? 1u : 0u);
+                }
+                mma_commit(bar(Lay::bSFull + g));
+                const int lo = g ? t.lo[1] : t.lo[0], hi = g ? t.hi[1] : t.hi[0];
+                owed[g] = (tile == lo ? 1 : 2) + (tile == hi - 1 ? 4 : 0);
+              }
+            }
+          }
+          if (!ok) break;
+          mma_commit(bar(Lay::bKEmpty + ks));
+          if (++ks == kChunkKStages) {
+            ks = 0;
+            kphase ^= 1;
+          }
+          if (v_owed) {
+            mma_commit(bar(Lay::bVEmpty + vs));
+            if (++vs == kChunkVStages) {
+              vs = 0;
+              vphase ^= 1;
+            }
+          }
+          v_owed = true;
+        }
+        if (ok) mma_commit(bar(Lay::bQEmpty));
+        ++item;
+      }
+      bool v_waited = false;
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (ok && owed[g]) {
+          ok = product(g, !v_waited);
+          v_waited = true;
+        }
+    }
+  } else if (warp < 8) {
+    // ----------------------------------------------------------------- softmax
+    setmaxnreg_inc<kChunkSoftmaxRegs>();
+    const int g = warp >> 2;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // row of the query tile = TMEM lane
+    const int tr = r / group;           // its token in the tile (tpt or more: a row of zeros)
+    const int head_in = r - tr * group;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_cols = Lay::tS + g * 128;
+    const uint32_t o_cols = Lay::tO + g * D;
+    const uint64_t c2 = f2_pack(scale_log2, scale_log2);
+    bool ok = true;
+    uint32_t sphase = 0, ophase = 0;
+    int vi = 0;  // V tiles of the CTA before this item
+    for (Walk w(c, tpi, max_q, wl, wr, bounds); w.more && ok;
+         w.next(c, tpi, max_q, wl, wr)) {
+      const int tok0 = (2 * w.at.p + g) * tpt;  // first token of the query tile
+      const int off = w.seq.nk - w.seq.n;
+      int lo = 0, hi = 0, first = 0;
+      if (w.j1 > w.j0) {
+        const ChunkTiles t(w, tpt, wl, wr);
+        lo = g ? t.lo[1] : t.lo[0];
+        hi = g ? t.hi[1] : t.hi[0];
+        first = t.first;
+      }
+      // keys that every row of the query tile sees, and this thread's row
+      const int all_lo = min(tok0 + tpt, w.seq.n) - 1 + off - wl;
+      const int all_hi = min(w.seq.nk - 1, tok0 + off + wr);
+      const int mid = tok0 + tr + off;
+      const int row_lo = mid - wl, row_hi = min(w.seq.nk - 1, mid + wr);
+      float m = -INFINITY;  // running reference, base-2 scaled units
+      float l = 0.f;        // row sum of p
+      float l_o = 0.f;      // row sum of the 16-bit-rounded p
+      for (int tile = lo; tile < hi; ++tile) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bSFull + g), sphase, abort_flag));
+        if (!ok) break;
+        sphase ^= 1;
+        tc_fence_after();
+        float s[128];
+        {
+          uint32_t sr[128];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(lane_base + s_cols + i * 32, sr + i * 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) reg_fence32(sr + i * 32);
+#pragma unroll
+          for (int e = 0; e < 128; ++e) s[e] = __uint_as_float(sr[e]);
+        }
+        const int key0 = tile * kKeyTile;
+        const bool edge = key0 < all_lo || key0 + kKeyTile - 1 > all_hi;
+        if (edge) {
+          const int first_col = row_lo - key0, last_col = row_hi - key0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            s[i] = (i > last_col || i < first_col) ? -INFINITY : s[i];
+          const int key = key0 + r;
+          if (key0 < w.keys.lo || key0 + kKeyTile - 1 > w.keys.hi) {  // the same for all threads
+            const int v = vi + tile - first;
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(bar(Lay::bVFull + v % kChunkVStages),
+                                      static_cast<uint32_t>(v / kChunkVStages) & 1, abort_flag));
+            if (!ok) break;
+            if (key < w.keys.lo || key > w.keys.hi) {
+              const uint32_t row =
+                  sbase + Lay::kV + (v % kChunkVStages) * Lay::kTileBytes + r * 128;
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 row + (i >> 3) * Lay::kChunkBytes + (i & 7) * 16),
+                             "r"(0)
+                             : "memory");
+            }
+            fence_async_smem();
+          }
+        }
+        // row maximum over four independent chains
+        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; i += 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mq[k] = fmax3(mq[k], s[i + 2 * k], s[i + 2 * k + 1]);
+        }
+        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        const float cand = mx * scale_log2;
+        const float m_new = (cand > m + kChunkRescaleSlack) ? cand : m;
+        // a row that has seen no key keeps m = -inf: alpha = 1, and 0 is subtracted
+        const bool empty_row = m_new == -INFINITY;
+        const float alpha = empty_row ? 1.f : ex2_approx(m - m_new);  // 0 at first
+        const float m_sub = empty_row ? 0.f : m_new;
+        const uint64_t nm2 = f2_pack(-m_sub, -m_sub);
+        auto rescale_o = [&]() {
+          if (tile > lo && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t o[32];
+              tmem_ld32(lane_base + o_cols + i * 32, o);
+              tmem_wait_ld();
+              reg_fence32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(lane_base + o_cols + i * 32, o);
+            }
+          }
+        };
+        if (kSplitPV) rescale_o();
+        uint64_t sum2[2] = {0, 0}, sum2_o[2] = {0, 0};  // packed +0.0f
+        auto exps = [&](auto poly_tag) {
+          constexpr bool kPoly = decltype(poly_tag)::value;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int e = h * 32 + 2 * i;
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, nm2), x0, x1);
+              float p0, p1;
+              if (kPoly && i % kPolyStride == kPolyStride - 1) {
+                ex2_poly_pair(x0, x1, p0, p1);
+              } else {
+                p0 = ex2_approx(x0);
+                p1 = ex2_approx(x1);
+              }
+              pk[i] = pack2<BF16>(p0, p1);
+              float r0, r1;
+              unpack2<BF16>(pk[i], r0, r1);
+              sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
+              sum2_o[i & 1] = f2_add(sum2_o[i & 1], f2_pack(r0, r1));
+            }
+            tmem_st16(lane_base + s_cols + h * 16, pk);
+            if (kSplitPV && h == 1) {  // keys 0-63 (and a rescaled O) are in TMEM
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(bar(Lay::bPHalf + g));
+            }
+          }
+        };
+        // masked tiles stay on the MUFU, which returns exact zeros for them
+        if (kPolyPairs > 0 && !edge)
+          exps(std::integral_constant<bool, true>{});
+        else
+          exps(std::integral_constant<bool, false>{});
+        float a0, a1, b0, b1;
+        f2_unpack(f2_add(sum2[0], sum2[1]), a0, a1);
+        f2_unpack(f2_add(sum2_o[0], sum2_o[1]), b0, b1);
+        l = l * alpha + (a0 + a1);
+        l_o = l_o * alpha + (b0 + b1);
+        if (!kSplitPV) rescale_o();
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(Lay::bPFull + g));
+        m = m_new;
+      }
+      vi += w.j1 - w.j0;
+      // O / l_o straight from the row's thread to its place
+      if (hi > lo) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(Lay::bODone + g), ophase, abort_flag));
+        if (!ok) break;
+        ophase ^= 1;
+        tc_fence_after();
+      }
+      const int ti = tok0 + tr;
+      const bool live = tr < tpt && ti < w.seq.n;
+      const bool whole = w.j0 == 0 && w.j1 == w.keys.count;
+      const long prow = (w.j0 > 0 ? 2L * blockIdx.x : 2L * blockIdx.x + 1) * kChunkRows +
+                        (g * tpt + tr) * group + head_in;
+      const int head = w.at.h * group + head_in;
+      const long orow = w.seq.begin + ti;
+      uint16_t* dst = O + orow * so.sn + head * so.sh;
+      float* part = Opart + prow * D;
+      const float inv_l = l_o > 0.f ? 1.f / l_o : 0.f;  // rows that see no key: O = 0
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[32];
+        if (hi > lo) {  // without a key tile O was never written
+          tmem_ld32(lane_base + o_cols + i * 32, o);
+          tmem_wait_ld();
+          reg_fence32(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (live && whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t hw[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              hw[k] = pack2<BF16>(__uint_as_float(o[8 * e + 2 * k]) * inv_l,
+                                  __uint_as_float(o[8 * e + 2 * k + 1]) * inv_l);
+            *reinterpret_cast<uint4*>(dst + i * 32 + e * 8) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+          }
+        } else if (live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(part + i * 32 + e * 4) =
+                make_float4(__uint_as_float(o[4 * e]) * inv_l, __uint_as_float(o[4 * e + 1]) * inv_l,
+                            __uint_as_float(o[4 * e + 2]) * inv_l,
+                            __uint_as_float(o[4 * e + 3]) * inv_l);
+        }
+      }
+      tc_fence_before();
+      if (live) {
+        const float L2 = l > 0.f ? m + log2f(l) : -INFINITY;
+        if (whole)
+          L[static_cast<long>(head) * c.tokens + orow] = L2 * 0.69314718055994530942f;
+        else
+          Lpart[prow] = L2;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kChunkMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace fa
