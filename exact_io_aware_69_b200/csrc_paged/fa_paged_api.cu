@@ -31,7 +31,23 @@ fa::Strides strides(const fa_strides& s) {
   return {static_cast<long>(s.b), static_cast<long>(s.h), static_cast<long>(s.n)};
 }
 
-int launch_status() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+// Launches a kernel so that it may begin before the one ahead of it in the stream has
+// ended: every kernel here waits for that end itself before it touches memory.
+template <typename... Params, typename... Args>
+int launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+           const Args&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
 
 // ------------------------------------------------------------------ rotation
 int check_rotation(int d, int rot_dim, float magnitude, const double* freqs) {
@@ -57,13 +73,9 @@ int launch_rope(fa::RopeArgs& a, bool interleaved, int dtype, cudaStream_t strea
   const long blocks = (a.rows + a.tokens_per_block - 1) / a.tokens_per_block;
   if (blocks >= (1L << 31)) return FA_ERR_UNSUPPORTED;
   const size_t smem = static_cast<size_t>(a.tokens_per_block) * a.rot * sizeof(float);
-  if (dtype == FA_BF16)
-    fa::fa_rope_kernel<PAGED, true>
-        <<<static_cast<unsigned>(blocks), fa::kRopeThreads, smem, stream>>>(a, interleaved);
-  else
-    fa::fa_rope_kernel<PAGED, false>
-        <<<static_cast<unsigned>(blocks), fa::kRopeThreads, smem, stream>>>(a, interleaved);
-  return launch_status();
+  const dim3 grid(static_cast<unsigned>(blocks));
+  return launch(dtype == FA_BF16 ? fa::fa_rope_kernel<PAGED, true> : fa::fa_rope_kernel<PAGED, false>,
+                grid, fa::kRopeThreads, smem, stream, a, interleaved);
 }
 
 fa::RopeRows rope_rows(const void* x, const fa_strides& xs, void* y, const fa_strides& ys,
@@ -106,9 +118,7 @@ fa::PagedView view_of(const fa_paged_cache& c) {
 int edge(int w) { return w < 0 || w >= fa::kUnbounded ? fa::kUnbounded : w; }
 
 // ----------------------------------------------------------------- attention
-// CTAs of an attention launch: one per SM of a B200. A fixed count keeps the split -- and
-// so the rounding where parts are joined -- the same everywhere.
-constexpr int kGrid = 148;
+constexpr int kGrid = fa::kSplitGrid;
 constexpr size_t kMaxDynSmem = 232448;  // 227 KB per block on sm_100
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -204,31 +214,19 @@ bool make_maps(const AttentionArgs& a, int tokens, CUtensorMap* q, CUtensorMap* 
                    {c.v_row, c.v_head, c.v_page}, rows, 1);
 }
 
-// Joins the parts; launched so that it may begin while the kernel before it still runs
-// (it waits for that kernel's end before it reads anything).
+// Joins the parts of items of up to `rows` rows.
 template <int D, int WPR, bool BF16>
-int launch_merge(const AttentionArgs& a) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kGrid, static_cast<unsigned>(a.ws.rows * WPR * 32 / fa::kMergeThreads));
-  cfg.blockDim = dim3(fa::kMergeThreads);
-  cfg.stream = a.stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, WPR, BF16>,
-                            static_cast<const float*>(a.opart()),
-                            static_cast<const float*>(a.lpart()),
-                            static_cast<const fa::PartInfo*>(a.parts()), kGrid, a.ws.rows, a.group,
-                            static_cast<uint16_t*>(a.O), strides(a.xo), a.L,
-                            a.c->tokens) == cudaSuccess
-             ? FA_OK
-             : FA_ERR_CUDA;
+int launch_merge(const AttentionArgs& a, int rows) {
+  constexpr int kRows = fa::kMergeThreads / 32 / WPR;
+  const dim3 grid(kGrid, static_cast<unsigned>((rows + kRows - 1) / kRows));
+  return launch(fa::fa_paged_merge_kernel<D, WPR, BF16>, grid, fa::kMergeThreads, 0, a.stream,
+                static_cast<const float*>(a.opart()), static_cast<const float*>(a.lpart()),
+                static_cast<const fa::PartInfo*>(a.parts()), a.ws.rows, a.group,
+                static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.c->tokens);
 }
 
 // The least cost (in key tiles) that is worth a CTA of its own.
-constexpr int kStepLeast = 4;
+constexpr int kStepLeast = 2;
 
 template <int D, int NQ, bool BF16>
 int launch_step(const AttentionArgs& a) {
@@ -240,11 +238,11 @@ int launch_step(const AttentionArgs& a) {
     return FA_ERR_CUDA;
   CUtensorMap q, k, v;
   if (!make_maps(a, a.max_q, &q, &k, &v)) return FA_ERR_CUDA;
-  kern<<<kGrid, Lay::kThreads, Lay::kBytes, a.stream>>>(
-      q, k, v, view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.opart(),
-      a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kStepLeast, a.scale * kLog2e);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  return launch_merge<D, 8, BF16>(a);
+  const int st = launch(kern, dim3(kGrid), Lay::kThreads, Lay::kBytes, a.stream, q, k, v,
+                        view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.opart(),
+                        a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kStepLeast,
+                        a.scale * kLog2e);
+  return st != FA_OK ? st : launch_merge<D, 8, BF16>(a, a.max_q * a.group);
 }
 
 // ... and for chunks, whose tiles take longer and whose parts are larger.
@@ -265,11 +263,11 @@ int launch_chunk(const AttentionArgs& a) {
   if (attr.numRegs != fa::kChunkLaunchRegs) return FA_ERR_UNSUPPORTED;
   CUtensorMap q, k, v;
   if (!make_maps(a, fa::kKeyTile / a.group, &q, &k, &v)) return FA_ERR_CUDA;
-  kern<<<kGrid, fa::kChunkThreads, Lay::kSmem, a.stream>>>(
-      q, k, v, view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.opart(),
-      a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kChunkLeast, a.scale * kLog2e);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  return launch_merge<D, 1, BF16>(a);
+  const int st = launch(kern, dim3(kGrid), fa::kChunkThreads, Lay::kSmem, a.stream, q, k, v,
+                        view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.opart(),
+                        a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kChunkLeast,
+                        a.scale * kLog2e);
+  return st != FA_OK ? st : launch_merge<D, 1, BF16>(a, fa::kChunkRows);
 }
 
 template <int D, bool BF16>

@@ -60,7 +60,7 @@ struct ChunkLayout {
   static constexpr uint32_t kK = kQ + 2 * kTileBytes;
   static constexpr uint32_t kV = kK + kChunkKStages * kTileBytes;
   static constexpr uint32_t kBounds = kV + kChunkVStages * kTileBytes;
-  static constexpr uint32_t kBar = kBounds + 32;
+  static constexpr uint32_t kBar = kBounds + sizeof(Stretch);
   static constexpr int bQFull = 0, bQEmpty = 1, bKFull = 2, bKEmpty = bKFull + kChunkKStages,
                        bVFull = bKEmpty + kChunkKStages, bVEmpty = bVFull + kChunkVStages,
                        bSFull = bVEmpty + kChunkVStages, bPFull = bSFull + 2,
@@ -128,9 +128,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int tpi = 2 * tpt;           // tokens of an item
   auto bar = [&](int i) -> uint32_t { return sbase + Lay::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbort);
-  Bound* bounds = reinterpret_cast<Bound*>(smem + Lay::kBounds);
+  Stretch* bounds = reinterpret_cast<Stretch*>(smem + Lay::kBounds);
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  dependents_may_launch();
   if (threadIdx.x == 0) {
     mbar_init(bar(Lay::bQFull), 1);
     mbar_init(bar(Lay::bQEmpty), 1);
@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   for (uint32_t i = threadIdx.x; i < 2 * Lay::kTileBytes / 16; i += kChunkThreads)
     *reinterpret_cast<uint4*>(smem + Lay::kQ + i * 16) = make_uint4(0u, 0u, 0u, 0u);
   tc_fence_before();
+  dependency_wait();
   split_bounds<false>(c, tpi, max_q, wl, wr, least,
                       reinterpret_cast<long long*>(smem + Lay::kK), bounds);
   tc_fence_after();
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     bool ok = true;
     PageWindow win;
     win.bad = false;
-    for (Walk w(c, tpi, max_q, wl, wr, bounds); w.more && ok;
+    for (Walk w(c, tpi, max_q, wl, wr, *bounds); w.more && ok;
          w.next(c, tpi, max_q, wl, wr)) {
       if (w.j0 >= w.j1) continue;
       const int first = w.keys.first + w.j0;
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
     if (win.bad) atomicExch(&g_fa_status, kStatusInvalid);
-    if (is_k && lane == 0) write_part_info(c, tpi, max_q, bounds, parts);
+    if (is_k && lane == 0) write_part_info(c, tpi, max_q, *bounds, parts);
   } else if (warp == kChunkMmaWarp) {
     // -------------------------------------------------------------- MMA issuer
     if (lane == 0) {
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         return true;
       };
       bool v_owed = false;  // the previous tile's V stage is to be released
-      for (Walk w(c, tpi, max_q, wl, wr, bounds); w.more && ok;
+      for (Walk w(c, tpi, max_q, wl, wr, *bounds); w.more && ok;
            w.next(c, tpi, max_q, wl, wr)) {
         if (w.j0 >= w.j1) continue;
         const ChunkTiles t(w, tpt, wl, wr);
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     bool ok = true;
     uint32_t sphase = 0, ophase = 0;
     int vi = 0;  // V tiles of the CTA before this item
-    for (Walk w(c, tpi, max_q, wl, wr, bounds); w.more && ok;
+    for (Walk w(c, tpi, max_q, wl, wr, *bounds); w.more && ok;
          w.next(c, tpi, max_q, wl, wr)) {
       const int tok0 = (2 * w.at.p + g) * tpt;  // first token of the query tile
       const int off = w.seq.nk - w.seq.n;

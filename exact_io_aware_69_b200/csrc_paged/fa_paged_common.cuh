@@ -9,6 +9,16 @@ namespace fa {
 
 constexpr int kStatusInvalid = -1;  // == FA_ERR_INVALID
 
+// Dependent launch: a kernel's launch overlaps the end of the one before it, and nothing of
+// what that one wrote (or still reads) is touched before dependency_wait. Every thread
+// waits, so a kernel has ended only when all before it have.
+__device__ __forceinline__ void dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void dependents_may_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 struct PagedView {
   const int* table;
   const int* cu_q;
@@ -45,10 +55,37 @@ __device__ __forceinline__ float warp_max(float x) {
   for (int s = 16; s >= 1; s >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
   return x;
 }
-__device__ __forceinline__ float warp_sum(float x) {
+// Reduces C (16 or 32) columns over the 32 lanes at once: v[q] is this lane's value of
+// column q; the result is that of column lane % C. Each round halves the columns a lane
+// keeps, so C columns take about C shuffles instead of 5 C.
+struct MaxOf {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct SumOf {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+template <int C, class Op>
+__device__ __forceinline__ float reduce_columns(float* v, int lane, Op op) {
 #pragma unroll
-  for (int s = 16; s >= 1; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-  return x;
+  for (int s = C / 2; s >= 1; s >>= 1) {
+    const bool upper = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float send = upper ? v[i] : v[i + s];
+      const float keep = upper ? v[i + s] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, s));
+    }
+  }
+  if (C == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+  return v[0];
+}
+// Four consecutive 32-bit TMEM columns of this warp's lanes.
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+  tmem_wait_ld();
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]));
 }
 // Named barrier over `count` threads that tells each whether any of them passed true.
 __device__ __forceinline__ bool named_bar_or(int id, int count, bool v) {

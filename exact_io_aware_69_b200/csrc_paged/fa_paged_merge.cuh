@@ -16,26 +16,29 @@
 namespace fa {
 
 constexpr int kMergeThreads = 256;
+static_assert(kMergeThreads >= kSplitGrid, "one thread per CTA of the split");
 
 template <int D, int WPR, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads)
     fa_paged_merge_kernel(const float* __restrict__ Opart, const float* __restrict__ Lpart,
-                          const PartInfo* __restrict__ parts, int grid, int rows_per_slot,
-                          int group, uint16_t* __restrict__ O, Strides so, float* __restrict__ L,
+                          const PartInfo* __restrict__ parts, int rows_per_slot, int group,
+                          uint16_t* __restrict__ O, Strides so, float* __restrict__ L,
                           int tokens) {
   constexpr int CPL = D / 32;
   constexpr int kRows = kMergeThreads / 32 / WPR;  // rows of a block
   __shared__ int last;                             // the CTA of the item's last part
   __shared__ float s_m[8], s_l[8], s_o[8][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) last = kSplitGrid - 1;
+  dependents_may_launch();
+  dependency_wait();
+  const int i = c + 1 + static_cast<int>(threadIdx.x);
+  const bool goes_on = i < kSplitGrid && parts[i].goes_on;  // loaded beside the next line's
   const PartInfo info = parts[c];
   if (!info.begins) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) last = grid - 1;
   __syncthreads();
-  for (int i = c + 1 + static_cast<int>(threadIdx.x); i < grid; i += kMergeThreads)
-    if (!parts[i].goes_on) atomicMin(&last, i);
+  if (i < kSplitGrid && !goes_on) atomicMin(&last, i);
   __syncthreads();
   const int n = last - c + 1;  // parts: slot 2 c + 1, then slots 2 (c + 1), 2 (c + 2), ...
   const int r = blockIdx.y * kRows + warp / WPR;

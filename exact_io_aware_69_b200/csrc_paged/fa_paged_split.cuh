@@ -46,14 +46,22 @@ __host__ __device__ inline KeyRange item_keys(int p, int tpi, int n, int nk, int
 __host__ __device__ inline int items_of(int n, int tpi) { return (n + tpi - 1) / tpi; }
 __host__ __device__ inline int item_cost(const KeyRange& r) { return r.count + kItemCost; }
 
-// CTAs that share cost W: no more than the grid, and no CTA with less than `least`.
-__host__ __device__ inline int split_active(long long W, int grid, int least) {
-  const long long most = W / least;
-  return most < 1 ? 1 : most < grid ? static_cast<int>(most) : grid;
+// CTAs of an attention launch: one per SM of a B200. A fixed count keeps the split the
+// same everywhere, and divisions by it are multiplications.
+constexpr int kSplitGrid = 148;
+// A CTA's share of cost W: an even part of it, at least `least`. (Every CTA computes it in
+// its prologue, where a 64-bit division by a variable is 400 cycles of latency.)
+__host__ __device__ inline long long split_share(long long W, int least) {
+  const long long even = (W + kSplitGrid - 1) / kSplitGrid;
+  return even > least ? even : least;
 }
 // Start of CTA c's stretch.
-__host__ __device__ inline long long split_start(long long W, int c, int active) {
-  return W / active * c + W % active * c / active;
+__host__ __device__ inline long long split_start(long long W, int c, long long share) {
+  return c * share < W ? c * share : W;
+}
+// a / b of non-negative numbers, 32 bits wide where they fit.
+__host__ __device__ inline long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : static_cast<unsigned>(a) / static_cast<unsigned>(b);
 }
 // The tile at which a boundary `r` units into an item cuts it (0: before the item).
 __host__ __device__ inline int split_tile(long long r) {
@@ -66,16 +74,17 @@ struct Bound {
 };
 
 #ifdef __CUDACC__
-__device__ __forceinline__ long long shfl_up64(long long v, int d) {
-  return __shfl_up_sync(0xffffffffu, v, d);
-}
+// A CTA's stretch: from `at` to before `end`; `seq` is at's sequence.
+struct Stretch {
+  Bound at, end;
+  SeqInfo seq;
+};
 
 // Called by all threads of the block. `costs`: shared scratch of 8 bytes per sequence;
-// bounds[0 .. 1]: shared, this CTA's stretch (empty when this CTA takes no part). Reports
-// sequences with inconsistent lengths. Ends with a __syncthreads.
+// *out: shared. Reports sequences with inconsistent lengths. Ends with a __syncthreads.
 template <bool ONE_ITEM>
 __device__ __forceinline__ void split_bounds(const PagedView& c, int tpi, int max_q, int wl,
-                                             int wr, int least, long long* costs, Bound* bounds) {
+                                             int wr, int least, long long* costs, Stretch* out) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5;
   // cost per key head of every sequence
@@ -107,14 +116,14 @@ __device__ __forceinline__ void split_bounds(const PagedView& c, int tpi, int ma
     long long upto = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long v = shfl_up64(upto, d);
+      const long long v = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += v;
     }
     const long long W = __shfl_sync(0xffffffffu, upto, 31) * c.heads;
-    const int active = split_active(W, gridDim.x, least);
-    const int me = static_cast<int>(blockIdx.x) + warp;
-    const long long x = me < active ? split_start(W, me, active) : W;
+    const long long x =
+        split_start(W, static_cast<int>(blockIdx.x) + warp, split_share(W, least));
     Bound at{c.batch, 0, 0, 0};
+    SeqInfo s{};
     if (x < W) {
       // the lane whose sequences hold x, then the sequence
       const long long before = (upto - own) * c.heads;
@@ -128,10 +137,10 @@ __device__ __forceinline__ void split_bounds(const PagedView& c, int tpi, int ma
       rem = __shfl_sync(0xffffffffu, rem, from);
       const long long w = costs[b];
       at.b = b;
-      at.h = static_cast<int>(rem / w);
+      at.h = static_cast<int>(quotient(rem, w));
       rem -= at.h * w;
+      s = seq_info(c, b, max_q);
       if (!ONE_ITEM) {
-        const SeqInfo s = seq_info(c, b, max_q);
         for (int p0 = 0;; p0 += 32) {  // ends: rem < w, the sum over all items
           const int p = p0 + lane;
           const bool real = p < items_of(s.n, tpi);
@@ -155,7 +164,14 @@ __device__ __forceinline__ void split_bounds(const PagedView& c, int tpi, int ma
       }
       at.j = split_tile(rem);
     }
-    if (lane == 0) bounds[warp] = at;
+    if (lane == 0) {
+      if (warp == 0) {
+        out->at = at;
+        out->seq = s;
+      } else {
+        out->end = at;
+      }
+    }
   }
   fence_async_smem();  // the scratch may be written by TMA next
   __syncthreads();
@@ -170,11 +186,10 @@ struct Walk {
   bool more;
 
   __device__ __forceinline__ Walk(const PagedView& c, int tpi, int max_q, int wl, int wr,
-                                  const Bound* bounds)
-      : at(bounds[0]), end(bounds[1]) {
+                                  const Stretch& s)
+      : at(s.at), end(s.end), seq(s.seq) {
     j0 = at.j;
     more = at.b < c.batch;
-    if (more) seq = seq_info(c, at.b, max_q);
     settle(c, tpi, wl, wr);
   }
   __device__ __forceinline__ bool at_end() const {
@@ -222,8 +237,8 @@ struct PartInfo {
 };
 
 __device__ __forceinline__ void write_part_info(const PagedView& c, int tpi, int max_q,
-                                                const Bound* bounds, PartInfo* parts) {
-  const Bound a = bounds[0], e = bounds[1];
+                                                const Stretch& stretch, PartInfo* parts) {
+  const Bound a = stretch.at, e = stretch.end;
   PartInfo info{};
   const bool same = a.b == e.b && a.h == e.h && a.p == e.p;
   if (a.b < c.batch && e.b < c.batch && e.j > 0 && !(same && e.j <= a.j)) {

@@ -20,7 +20,7 @@
 // Softmax: thread r of a warpgroup owns key r of the tile and 16 or 32 query columns. The
 // reference m of a column moves only when a score exceeds it by more than 2^8; whether
 // any does is one barrier-vote per tile, and only then are the tile's maxima exchanged and
-// O^T rescaled. Two sums per column: of the 16-bit weights, which normalises O, and of the
+// O^T rescaled. Columns beyond the item's rows are skipped in fours. Two sums per column: of the 16-bit weights, which normalises O, and of the
 // unrounded ones, which gives L.
 //
 // V rows of keys that no row of the item sees -- behind the sequence's end, before its
@@ -41,7 +41,7 @@ struct StepLayout {
   static constexpr int kGroups = NQ == 64 ? 2 : 1;  // softmax warpgroups
   static constexpr int kCols = NQ / kGroups;        // query columns of a softmax thread
   static constexpr int kSoftmax = 128 * kGroups;
-  static constexpr int kThreads = kSoftmax + 64;
+  static constexpr int kThreads = kSoftmax + 96;
   static constexpr uint32_t kTileBytes = kKeyTile * D * 2;
   static constexpr uint32_t kChunkBytes = kKeyTile * 128;  // 128 rows x 64 values
   static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // V tile, then K tile
@@ -51,11 +51,12 @@ struct StepLayout {
   static constexpr uint32_t kPBytes = NQ * 256;  // NQ rows x 128 keys
   static constexpr uint32_t kQ = kStages * kStageBytes;   // 2 buffers
   static constexpr uint32_t kP = kQ + 2 * kQBytes;        // 2 buffers
-  static constexpr uint32_t kRed = kP + 2 * kPBytes;      // [group][warp][column] maxima
-  static constexpr uint32_t kSums = kRed + 4 * NQ * 4;    // [group][warp][2][column]
-  static constexpr uint32_t kTok = kSums + 8 * NQ * 4;    // [column] token of a column
+  static constexpr uint32_t kRed = kP + 2 * kPBytes;      // [column][warp] maxima
+  static constexpr uint32_t kSums = kRed + 4 * NQ * 4;    // [2][column][warp]
+  static constexpr uint32_t kRef = kSums + 8 * NQ * 4;    // [column] reference
+  static constexpr uint32_t kTok = kRef + NQ * 4;         // [column] token of a column
   static constexpr uint32_t kBounds = kTok + NQ * 4;
-  static constexpr uint32_t kBar = kBounds + 32;
+  static constexpr uint32_t kBar = kBounds + sizeof(Stretch);
   static constexpr int kNumBars = 2 * kStages + 10;
   static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
   static constexpr uint32_t kAbort = kTmemSlot + 8;
@@ -147,13 +148,13 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return sbase + Lay::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbort);
   int* tok = reinterpret_cast<int*>(smem + Lay::kTok);
-  Bound* bounds = reinterpret_cast<Bound*>(smem + Lay::kBounds);
-  constexpr int kProducer = Lay::kSoftmax / 32, kMma = kProducer + 1;
+  Stretch* bounds = reinterpret_cast<Stretch*>(smem + Lay::kBounds);
+  constexpr int kProducer = Lay::kSoftmax / 32, kMma = kProducer + 2;  // K, V, MMA
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  dependents_may_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(bar(Lay::bFull + s), 1);
+      mbar_init(bar(Lay::bFull + s), 2);  // K and V
       mbar_init(bar(Lay::bEmpty + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -175,39 +176,44 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
     *reinterpret_cast<uint4*>(smem + Lay::kQ + i * 16) = make_uint4(0u, 0u, 0u, 0u);
   if (threadIdx.x < NQ) tok[threadIdx.x] = threadIdx.x / group;
   tc_fence_before();
+  dependency_wait();
   split_bounds<true>(c, max_q, max_q, wl, wr, least, reinterpret_cast<long long*>(smem), bounds);
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Lay::kTmemSlot);
-  Walk w(c, max_q, max_q, wl, wr, bounds);
+  Walk w(c, max_q, max_q, wl, wr, *bounds);
 
-  if (warp == kProducer) {
-    // ------------------------------------------------------------ TMA producer
+  if (warp == kProducer || warp == kProducer + 1) {
+    // --------------------------------------- TMA producers: Q and K, V
+    const bool is_k = warp == kProducer;
+    const CUtensorMap* map = is_k ? &tmK : &tmV;
     if (lane == 0) {
-      tma_prefetch(&tmQ);
-      tma_prefetch(&tmK);
-      tma_prefetch(&tmV);
-      write_part_info(c, max_q, max_q, bounds, parts);
+      tma_prefetch(map);
+      if (is_k) tma_prefetch(&tmQ);
     }
     __syncwarp();
     const uint32_t q_bytes = static_cast<uint32_t>(group) * max_q * D * 2;
+    const uint32_t at = sbase + (is_k ? Lay::kTileBytes : 0);
     int it = 0, item = 0;
     bool ok = true;
     PageWindow win;
     win.bad = false;
     for (; w.more && ok; w.next(c, max_q, max_q, wl, wr)) {
       if (w.j0 >= w.j1) continue;
-      const int qb = item & 1;
-      ok = item < 2 || mbar_wait(bar(Lay::bQEmpty + qb), static_cast<uint32_t>(item / 2 - 1) & 1,
-                                 abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) break;
       win.start(c, w.at.b, (w.keys.first + w.j0) * kKeyTile >> c.page_shift, lane);
-      if (lane == 0) {
-        mbar_expect_tx(bar(Lay::bQFull + qb), q_bytes);
-        for (int i = 0; i < D / 64; ++i)
-          tma_load_4d(sbase + Lay::kQ + qb * Lay::kQBytes + i * Lay::kQChunk, &tmQ, i * 64, 0,
-                      w.seq.begin, w.at.h, bar(Lay::bQFull + qb));
+      if (is_k) {
+        const int qb = item & 1;
+        ok = item < 2 || mbar_wait(bar(Lay::bQEmpty + qb),
+                                   static_cast<uint32_t>(item / 2 - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(Lay::bQFull + qb), q_bytes);
+          for (int i = 0; i < D / 64; ++i)
+            tma_load_4d(sbase + Lay::kQ + qb * Lay::kQBytes + i * Lay::kQChunk, &tmQ, i * 64, 0,
+                        w.seq.begin, w.at.h, bar(Lay::bQFull + qb));
+        }
+        __syncwarp();
+        ++item;
       }
-      ++item;
       for (int j = w.j0; j < w.j1; ++j, ++it) {
         const int st = it % S;
         const int tile = w.keys.first + j;
@@ -218,16 +224,16 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
           ok = false;
           break;
         }
-        const uint32_t dst = sbase + st * Lay::kStageBytes;
         if (lane == 0)
           mbar_expect_tx(bar(Lay::bFull + st),
-                         static_cast<uint32_t>(pages.count * pages.rows) * D * 4);
+                         static_cast<uint32_t>(pages.count * pages.rows) * D * 2);
         __syncwarp();
-        load_tile_pages<D>(pages, tile, c.page_shift, win, &tmV, dst, bar(Lay::bFull + st), &tmK,
-                           dst + Lay::kTileBytes, bar(Lay::bFull + st), w.at.h, lane);
+        load_tile_pages<D>(pages, tile, c.page_shift, win, map, at + st * Lay::kStageBytes,
+                           bar(Lay::bFull + st), nullptr, 0, 0, w.at.h, lane);
       }
     }
     if (win.bad) atomicExch(&g_fa_status, kStatusInvalid);
+    if (is_k && lane == 0) write_part_info(c, max_q, max_q, *bounds, parts);
   } else if (warp == kMma) {
     // -------------------------------------------------------------- MMA issuer
     if (lane == 0) {
@@ -282,31 +288,33 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
     }
   } else {
     // ----------------------------------------------------------------- softmax
-    const int wg = warp >> 2;           // columns wg * C .. wg * C + C - 1
-    const int r = threadIdx.x & 127;    // key of the tile = TMEM lane
+    const int wg = warp >> 2;         // columns wg * C .. wg * C + C - 1
+    const int r = threadIdx.x & 127;  // key of the tile = TMEM lane
     const int q0 = wg * C;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    float* red = reinterpret_cast<float*>(smem + Lay::kRed) + wg * 4 * C;
-    float* sums = reinterpret_cast<float*>(smem + Lay::kSums) + wg * 8 * C;
+    float* red = reinterpret_cast<float*>(smem + Lay::kRed) + q0 * 4;
+    float* sums = reinterpret_cast<float*>(smem + Lay::kSums) + q0 * 8;
+    float* refs = reinterpret_cast<float*>(smem + Lay::kRef) + q0;
     const int gbar = 1 + wg;
+    // a column that has seen no key: below every finite score, and -inf - kNone = -inf
+    constexpr float kNone = -3.402823466e38f;
     bool ok = true;
     int it = 0;
     for (; w.more && ok; w.next(c, max_q, max_q, wl, wr)) {
-      const int rows = w.seq.n * group;
+      const int cols = min(C, w.seq.n * group - q0);  // of this warpgroup, at least 1 in group 0
       const int off = w.seq.nk - w.seq.n;
       // keys that every row sees
       const int all_lo = w.seq.n - 1 + off - wl, all_hi = min(w.seq.nk - 1, off + wr);
       float m[C], l[C], l_o[C];
 #pragma unroll
       for (int q = 0; q < C; ++q) {
-        m[q] = -INFINITY;
+        m[q] = kNone;
         l[q] = 0.f;  // this thread's (key's) share of the sums
         l_o[q] = 0.f;
       }
       for (int j = w.j0; j < w.j1; ++j, ++it) {
         const int b = it & 1;
         const int key0 = (w.keys.first + j) * kKeyTile;
-        const int key = key0 + r;
         ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bSFull + b),
                                                static_cast<uint32_t>(it >> 1) & 1, abort_flag));
         float s[C];
@@ -316,10 +324,12 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
           uint32_t sr[C];
           tmem_ld_cols<C>(lane_base + b * NQ + q0, sr);
 #pragma unroll
-          for (int q = 0; q < C; ++q) s[q] = __uint_as_float(sr[q]) * scale_log2;
+          for (int q = 0; q < C; ++q) s[q] = __uint_as_float(sr[q]);
           if (key0 < all_lo || key0 + kKeyTile - 1 > all_hi) {  // an edge of the mask
+            const int key = key0 + r;
 #pragma unroll
             for (int q = 0; q < C; ++q) {
+              if ((q & 3) == 0 && q >= cols) break;
               const int mid = tok[q0 + q] + off;
               if (key > min(w.seq.nk - 1, mid + wr) || key < mid - wl) s[q] = -INFINITY;
             }
@@ -335,46 +345,56 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
             }
           }
 #pragma unroll
-          for (int q = 0; q < C; ++q) raise = raise || s[q] > m[q] + kStepRescaleSlack;
+          for (int q = 0; q < C; ++q) {
+            if ((q & 3) == 0 && q >= cols) break;
+            raise = raise || fmaf(s[q], scale_log2, -m[q]) > kStepRescaleSlack;
+          }
         }
         if (named_bar_or(gbar, 128, raise)) {
           ok = named_bar_and(gbar, 128, ok);
           if (!ok) break;
+          {
+            float v[C];
 #pragma unroll
-          for (int q = 0; q < C; ++q) {
-            const float mw = warp_max(s[q]);
-            if (lane == 0) red[(warp & 3) * C + q] = mw;
+            for (int q = 0; q < C; ++q) v[q] = s[q];
+            const float top = reduce_columns<C>(v, lane, MaxOf());
+            if (lane < C) red[lane * 4 + (warp & 3)] = top * scale_log2;
           }
           named_bar_sync(gbar, 128);
-          float alpha[C];
-#pragma unroll
-          for (int q = 0; q < C; ++q) {
-            const float top =
-                fmaxf(fmaxf(red[q], red[C + q]), fmaxf(red[2 * C + q], red[3 * C + q]));
-            const float m_new = top > m[q] + kStepRescaleSlack ? top : m[q];
-            alpha[q] = m_new == -INFINITY ? 1.f : ex2_approx(m[q] - m_new);  // 0 at first
-            m[q] = m_new;
-            l[q] *= alpha[q];
-            l_o[q] *= alpha[q];
-          }
-          if (j > w.j0) {  // O^T holds products: rescale it once the last one has landed
+          // O^T holds products: it is rescaled, once the last of them has landed
+          const bool rescale = j > w.j0;
+          if (rescale) {
             ok = __all_sync(0xffffffffu,
                             mbar_wait(bar(Lay::bDone + (b ^ 1)),
                                       static_cast<uint32_t>((it - 1) >> 1) & 1, abort_flag));
-            if (ok) {
-              tc_fence_after();
-              uint32_t o[C];
-              tmem_ld_cols<C>(lane_base + Lay::tO + q0, o);
+            tc_fence_after();
+          }
 #pragma unroll
-              for (int q = 0; q < C; ++q)
-                o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha[q]);
-              if constexpr (C == 16)
-                tmem_st16(lane_base + Lay::tO + q0, o);
-              else
-                tmem_st32(lane_base + Lay::tO + q0, o);
-              tmem_wait_st();
+          for (int q4 = 0; q4 < C; q4 += 4) {
+            if (q4 >= cols) break;
+            float alpha[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int q = q4 + k;
+              const float4 t = *reinterpret_cast<const float4*>(red + q * 4);
+              const float top = fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w));
+              const float m_new = top > m[q] + kStepRescaleSlack ? top : m[q];
+              alpha[k] = ex2_approx(m[q] - m_new);  // 0 at first
+              m[q] = m_new;
+              l[q] *= alpha[k];
+              l_o[q] *= alpha[k];
+            }
+            if (rescale && ok) {
+              uint32_t o[4];
+              tmem_ld4(lane_base + Lay::tO + q0 + q4, o);
+              tmem_st4(lane_base + Lay::tO + q0 + q4,
+                       __float_as_uint(__uint_as_float(o[0]) * alpha[0]),
+                       __float_as_uint(__uint_as_float(o[1]) * alpha[1]),
+                       __float_as_uint(__uint_as_float(o[2]) * alpha[2]),
+                       __float_as_uint(__uint_as_float(o[3]) * alpha[3]));
             }
           }
+          if (rescale) tmem_wait_st();
         }
         // P_j^T into buffer b, once the product before last has read it
         if (ok && it >= 2)
@@ -384,8 +404,8 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
         uint8_t* pt = smem + Lay::kP + b * Lay::kPBytes;
 #pragma unroll
         for (int q = 0; q < C; ++q) {
-          // a column that has seen no key yet has m = -inf and gets 0
-          const float p = m[q] == -INFINITY ? 0.f : ex2_approx(s[q] - m[q]);
+          if ((q & 3) == 0 && q >= cols) break;  // those rows of P are never read as a result
+          const float p = ex2_approx(fmaf(s[q], scale_log2, -m[q]));
           const uint32_t pk = pack2<BF16>(p, 0.f);
           float pr, unused;
           unpack2<BF16>(pk, pr, unused);
@@ -399,62 +419,67 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
         mbar_arrive(bar(Lay::bPFull + b));
         // a wait that gave up in one warp reaches the others at the next vote
       }
-      // the item's last product, and the sums over the tile's 128 keys
+      // sums over the tile's 128 keys, while the item's last product runs
+      {
+        const float a = reduce_columns<C>(l, lane, SumOf());
+        const float e = reduce_columns<C>(l_o, lane, SumOf());
+        if (lane < C) {
+          sums[lane * 8 + (warp & 3)] = a;
+          sums[lane * 8 + 4 + (warp & 3)] = e;
+        }
+        if (r == 0) {
+#pragma unroll
+          for (int q = 0; q < C; ++q) refs[q] = m[q];
+        }
+      }
       const bool some = w.j1 > w.j0;
       ok = __all_sync(0xffffffffu,
                       ok && (!some || mbar_wait(bar(Lay::bDone + ((it - 1) & 1)),
                                                 static_cast<uint32_t>((it - 1) >> 1) & 1,
                                                 abort_flag)));
-#pragma unroll
-      for (int q = 0; q < C; ++q) {
-        if (q0 + q < rows) {
-          const float a = warp_sum(l[q]), e = warp_sum(l_o[q]);
-          if (lane == 0) {
-            sums[((warp & 3) * 2 + 0) * C + q] = a;
-            sums[((warp & 3) * 2 + 1) * C + q] = e;
-          }
-        }
-      }
       ok = named_bar_and(gbar, 128, ok);
       if (!ok) break;
-      uint32_t o[C];
-      if (some) {
-        tc_fence_after();
-        tmem_ld_cols<C>(lane_base + Lay::tO + q0, o);
-        tc_fence_before();
-      } else {
-#pragma unroll
-        for (int q = 0; q < C; ++q) o[q] = 0u;
-      }
+      tc_fence_after();
       const bool whole = w.j0 == 0 && w.j1 == w.keys.count;
       const long slot = w.j0 > 0 ? 2L * blockIdx.x : 2L * blockIdx.x + 1;
+      // thread r: row r of the d columns (lane r of O^T) of every query column ...
+#pragma unroll 1
+      for (int q4 = 0; q4 < cols; q4 += 4) {
+        uint32_t o[4];
+        tmem_ld4(lane_base + Lay::tO + q0 + q4, o);
 #pragma unroll
-      for (int q = 0; q < C; ++q) {
-        if (q0 + q < rows) {
-          float a = 0.f, e = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a += sums[(i * 2 + 0) * C + q];
-            e += sums[(i * 2 + 1) * C + q];
-          }
-          const float val = e > 0.f ? __uint_as_float(o[q]) / e : 0.f;  // no key: O = 0
-          const float L2 = a > 0.f ? m[q] + log2f(a) : -INFINITY;
+        for (int k = 0; k < 4; ++k) {
+          const int q = q4 + k;
+          if (q >= cols || (D < 128 && r >= D)) break;
+          const float4 t = *reinterpret_cast<const float4*>(sums + q * 8 + 4);
+          const float e = (t.x + t.y) + (t.z + t.w);
+          // no key seen: O = 0 (and O^T may not have been written at all)
+          const float val = e > 0.f ? __fdividef(__uint_as_float(o[k]), e) : 0.f;
           if (whole) {
-            const int t = tok[q0 + q];
-            const int head = w.at.h * group + q0 + q - t * group;
-            const long row = w.seq.begin + t;
-            if (r < D)
-              O[row * so.sn + head * so.sh + r] =
-                  static_cast<uint16_t>(pack2<BF16>(val, 0.f) & 0xFFFFu);
-            if (r == 0)
-              L[static_cast<long>(head) * c.tokens + row] = L2 * 0.69314718055994530942f;
+            const int tq = tok[q0 + q];
+            const int head = w.at.h * group + q0 + q - tq * group;
+            O[(w.seq.begin + tq) * so.sn + head * so.sh + r] =
+                static_cast<uint16_t>(pack2<BF16>(val, 0.f) & 0xFFFFu);
           } else {
-            const long row = slot * NQ + q0 + q;
-            if (r < D) Opart[row * D + r] = val;
-            if (r == 0) Lpart[row] = L2;
+            Opart[(slot * NQ + q0 + q) * D + r] = val;
           }
         }
       }
+      // ... and L of query column r
+      if (r < cols) {
+        const float4 t = *reinterpret_cast<const float4*>(sums + r * 8);
+        const float a = (t.x + t.y) + (t.z + t.w);
+        const float L2 = a > 0.f ? refs[r] + log2f(a) : -INFINITY;
+        if (whole) {
+          const int tq = tok[q0 + r];
+          const int head = w.at.h * group + q0 + r - tq * group;
+          L[static_cast<long>(head) * c.tokens + w.seq.begin + tq] =
+              L2 * 0.69314718055994530942f;
+        } else {
+          Lpart[slot * NQ + q0 + r] = L2;
+        }
+      }
+      tc_fence_before();
       named_bar_sync(gbar, 128);  // the sums are read before the next item's are written
     }
   }

@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a,
   __shared__ int s_page[kRopeMaxTokens];   // append: destination page (-1: not written)
   __shared__ int s_row[kRopeMaxTokens];
 
+  dependents_may_launch();
+  dependency_wait();
   const int tpb = a.tokens_per_block;
   const long t0 = static_cast<long>(blockIdx.x) * tpb;
   const int nt = static_cast<int>(min(static_cast<long>(tpb), a.rows - t0));
