@@ -5,6 +5,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "fa_paged.h"
@@ -24,8 +25,8 @@ bool aligned(const void* p, uintptr_t bytes) {
 bool ok_ptr(const void* p, uintptr_t bytes = 16) { return p != nullptr && aligned(p, bytes); }
 
 // Rows are moved in 16-byte pieces, so every stride is a multiple of 8 elements.
-bool ok_strides(const fa_strides* s) {
-  return s != nullptr && s->b >= 0 && s->h >= 0 && s->n >= 0 && (s->b | s->h | s->n) % 8 == 0;
+bool ok_strides(const fa_strides& s) {
+  return s.b >= 0 && s.h >= 0 && s.n >= 0 && (s.b | s.h | s.n) % 8 == 0;
 }
 fa::Strides strides(const fa_strides& s) {
   return {static_cast<long>(s.b), static_cast<long>(s.h), static_cast<long>(s.n)};
@@ -78,15 +79,16 @@ int launch_rope(fa::RopeArgs& a, bool interleaved, int dtype, cudaStream_t strea
                 grid, fa::kRopeThreads, smem, stream, a, interleaved);
 }
 
-fa::RopeRows rope_rows(const void* x, const fa_strides& xs, void* y, const fa_strides& ys,
-                       int heads) {
-  return {static_cast<const uint16_t*>(x), static_cast<uint16_t*>(y), strides(xs), strides(ys),
-          heads};
+bool ok_rows(const fa_rope_rows& r) {
+  return r.heads == 0 || (ok_ptr(r.x) && ok_ptr(r.y) && ok_strides(r.xs) && ok_strides(r.ys));
+}
+fa::RopeRows rope_rows(const fa_rope_rows& r) {
+  return {static_cast<const uint16_t*>(r.x), static_cast<uint16_t*>(r.y), strides(r.xs),
+          strides(r.ys), r.heads};
 }
 
 // --------------------------------------------------------------------- cache
 int check_cache(const fa_paged_cache* c, bool attention) {
-  if (c == nullptr) return FA_ERR_INVALID;
   if (c->batch < 0 || c->tokens < 0 || c->heads <= 0 || c->d <= 0 || c->num_pages < 0 ||
       c->table_width < 0 || c->table_row < 0)
     return FA_ERR_INVALID;
@@ -103,7 +105,7 @@ int check_cache(const fa_paged_cache* c, bool attention) {
   if (c->table_width > 0 && !ok_ptr(c->table, 4)) return FA_ERR_INVALID;
   if (c->num_pages > 0 && (!ok_ptr(c->k_pages) || !ok_ptr(c->v_pages))) return FA_ERR_INVALID;
   const fa_strides k{c->k_page, c->k_head, c->k_row}, v{c->v_page, c->v_head, c->v_row};
-  if (!ok_strides(&k) || !ok_strides(&v)) return FA_ERR_INVALID;
+  if (!ok_strides(k) || !ok_strides(v)) return FA_ERR_INVALID;
   return FA_OK;
 }
 
@@ -225,6 +227,13 @@ int launch_merge(const AttentionArgs& a, int rows) {
                 static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.c->tokens);
 }
 
+// A kernel's shared-memory limit, set on every call: it is the current context's.
+template <typename Kernel>
+bool allow_smem(Kernel kernel, size_t smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(smem)) == cudaSuccess;
+}
+
 // The least cost (in key tiles) that is worth a CTA of its own.
 constexpr int kStepLeast = 2;
 
@@ -233,9 +242,7 @@ int launch_step(const AttentionArgs& a) {
   using Lay = fa::StepLayout<D, NQ>;
   static_assert(Lay::kBytes <= kMaxDynSmem, "shared memory");
   auto kern = fa::fa_paged_step_kernel<D, NQ, BF16>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(Lay::kBytes)) != cudaSuccess)
-    return FA_ERR_CUDA;
+  if (!allow_smem(kern, Lay::kBytes)) return FA_ERR_CUDA;
   CUtensorMap q, k, v;
   if (!make_maps(a, a.max_q, &q, &k, &v)) return FA_ERR_CUDA;
   const int st = launch(kern, dim3(kGrid), Lay::kThreads, Lay::kBytes, a.stream, q, k, v,
@@ -253,14 +260,16 @@ int launch_chunk(const AttentionArgs& a) {
   using Lay = fa::ChunkLayout<D>;
   static_assert(Lay::kSmem <= kMaxDynSmem, "shared memory");
   auto kern = fa::fa_paged_chunk_kernel<D, BF16>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(Lay::kSmem)) != cudaSuccess)
-    return FA_ERR_CUDA;
   // The kernel moves registers between warpgroups (setmaxnreg); its split adds up to
   // exactly 168 registers per thread at launch (the build fails otherwise too).
-  cudaFuncAttributes attr;
-  if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return FA_ERR_CUDA;
-  if (attr.numRegs != fa::kChunkLaunchRegs) return FA_ERR_UNSUPPORTED;
+  static std::atomic<bool> counted{false};
+  if (!counted.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return FA_ERR_CUDA;
+    if (attr.numRegs != fa::kChunkLaunchRegs) return FA_ERR_UNSUPPORTED;
+    counted.store(true, std::memory_order_relaxed);
+  }
+  if (!allow_smem(kern, Lay::kSmem)) return FA_ERR_CUDA;
   CUtensorMap q, k, v;
   if (!make_maps(a, fa::kKeyTile / a.group, &q, &k, &v)) return FA_ERR_CUDA;
   const int st = launch(kern, dim3(kGrid), fa::kChunkThreads, Lay::kSmem, a.stream, q, k, v,
@@ -284,117 +293,110 @@ int launch_attention(const AttentionArgs& a) {
 
 extern "C" {
 
-int fa_rope(const void* Xq, const fa_strides* xq, void* Yq, const fa_strides* yq, int Hq,
-            const void* Xk, const fa_strides* xk, void* Yk, const fa_strides* yk, int Hk,
-            const int* positions, long long pos_row, const double* freqs, int rot_dim,
-            float magnitude, int interleaved, int inverse, int B, int N, int d, int dtype,
-            void* stream) {
-  if (B < 0 || N < 0 || Hq < 0 || Hk < 0 || d <= 0 || pos_row < 0) return FA_ERR_INVALID;
-  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
-  if (d % 16 != 0 || d > fa::kRopeMaxDim) return FA_ERR_UNSUPPORTED;
-  const int st = check_rotation(d, rot_dim, magnitude, freqs);
+int fa_rope(const fa_rope_args* args, void* stream) {
+  if (args == nullptr) return FA_ERR_INVALID;
+  const fa_rope_args& r = *args;
+  if (r.batch < 0 || r.rows < 0 || r.q.heads < 0 || r.k.heads < 0 || r.d <= 0 || r.pos_row < 0)
+    return FA_ERR_INVALID;
+  if (r.dtype != FA_BF16 && r.dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
+  if (r.d % 16 != 0 || r.d > fa::kRopeMaxDim) return FA_ERR_UNSUPPORTED;
+  const int st = check_rotation(r.d, r.rot_dim, r.magnitude, r.freqs);
   if (st != FA_OK) return st;
-  if (static_cast<long long>(B) * N == 0 || Hq + Hk == 0) return FA_OK;
-  if (Hq > 0 && (!ok_ptr(Xq) || !ok_ptr(Yq) || !ok_strides(xq) || !ok_strides(yq)))
-    return FA_ERR_INVALID;
-  if (Hk > 0 && (!ok_ptr(Xk) || !ok_ptr(Yk) || !ok_strides(xk) || !ok_strides(yk)))
-    return FA_ERR_INVALID;
-  if (!aligned(positions, 4)) return FA_ERR_INVALID;
-  const fa_strides none{0, 0, 0};
+  if (static_cast<long long>(r.batch) * r.rows == 0 || r.q.heads + r.k.heads == 0) return FA_OK;
+  if (!ok_rows(r.q) || !ok_rows(r.k) || !aligned(r.positions, 4)) return FA_ERR_INVALID;
   fa::RopeArgs a{};
-  a.q = rope_rows(Xq, Hq ? *xq : none, Yq, Hq ? *yq : none, Hq);
-  a.k = rope_rows(Xk, Hk ? *xk : none, Yk, Hk ? *yk : none, Hk);
-  a.positions = positions;
-  a.pos_row = static_cast<long>(pos_row);
-  a.freqs = freqs;
-  a.rot = rot_dim;
-  a.d = d;
-  a.magnitude = magnitude;
-  a.sign = inverse ? -1.f : 1.f;
-  a.N = N;
-  a.rows = static_cast<long>(B) * N;
-  return launch_rope<false>(a, interleaved != 0, dtype, static_cast<cudaStream_t>(stream));
+  a.q = rope_rows(r.q);
+  a.k = rope_rows(r.k);
+  a.positions = r.positions;
+  a.pos_row = static_cast<long>(r.pos_row);
+  a.freqs = r.freqs;
+  a.rot = r.rot_dim;
+  a.d = r.d;
+  a.magnitude = r.magnitude;
+  a.sign = r.inverse ? -1.f : 1.f;
+  a.N = r.rows;
+  a.rows = static_cast<long>(r.batch) * r.rows;
+  return launch_rope<false>(a, r.interleaved != 0, r.dtype, static_cast<cudaStream_t>(stream));
 }
 
-int fa_paged_append(const fa_paged_cache* cache, const void* K, const fa_strides* xk,
-                    const void* V, const fa_strides* xv, const void* Xq, const fa_strides* xq,
-                    void* Yq, const fa_strides* yq, int Hq, const int* positions,
-                    const double* freqs, int rot_dim, float magnitude, int interleaved,
-                    void* stream) {
-  int st = check_cache(cache, false);
+int fa_paged_append(const fa_paged_append_args* args, void* stream) {
+  if (args == nullptr) return FA_ERR_INVALID;
+  const fa_paged_append_args& r = *args;
+  const fa_paged_cache& c = r.cache;
+  int st = check_cache(&c, false);
   if (st != FA_OK) return st;
-  if (Hq < 0 || (Hq > 0 && freqs == nullptr)) return FA_ERR_INVALID;
-  if (freqs != nullptr && (st = check_rotation(cache->d, rot_dim, magnitude, freqs)) != FA_OK)
+  if (r.q.heads < 0 || (r.q.heads > 0 && r.freqs == nullptr)) return FA_ERR_INVALID;
+  if (r.freqs != nullptr &&
+      (st = check_rotation(c.d, r.rot_dim, r.magnitude, r.freqs)) != FA_OK)
     return st;
-  if (cache->batch == 0 || cache->tokens == 0) return FA_OK;
-  if (!ok_ptr(K) || !ok_ptr(V) || !ok_strides(xk) || !ok_strides(xv)) return FA_ERR_INVALID;
-  if (Hq > 0 && (!ok_ptr(Xq) || !ok_ptr(Yq) || !ok_strides(xq) || !ok_strides(yq)))
+  if (c.batch == 0 || c.tokens == 0) return FA_OK;
+  if (!ok_ptr(r.k) || !ok_ptr(r.v) || !ok_strides(r.ks) || !ok_strides(r.vs) || !ok_rows(r.q) ||
+      !aligned(r.positions, 4))
     return FA_ERR_INVALID;
-  if (!aligned(positions, 4)) return FA_ERR_INVALID;
-  if (cache->num_pages == 0 || cache->table_width == 0) return FA_ERR_INVALID;
-  const fa_strides none{0, 0, 0}, kp{cache->k_page, cache->k_head, cache->k_row},
-      vp{cache->v_page, cache->v_head, cache->v_row};
+  if (c.num_pages == 0 || c.table_width == 0) return FA_ERR_INVALID;
+  const fa_strides kp{c.k_page, c.k_head, c.k_row}, vp{c.v_page, c.v_head, c.v_row};
   fa::RopeArgs a{};
-  a.q = rope_rows(Xq, Hq ? *xq : none, Yq, Hq ? *yq : none, Hq);
-  a.k = rope_rows(K, *xk, cache->k_pages, kp, cache->heads);
-  a.v = rope_rows(V, *xv, cache->v_pages, vp, cache->heads);
-  a.positions = positions;
-  a.freqs = freqs;
-  a.rot = freqs != nullptr ? rot_dim : 0;
-  a.d = cache->d;
-  a.magnitude = magnitude;
+  a.q = rope_rows(r.q);
+  a.k = rope_rows({r.k, c.k_pages, r.ks, kp, c.heads, 0});
+  a.v = rope_rows({r.v, c.v_pages, r.vs, vp, c.heads, 0});
+  a.positions = r.positions;
+  a.freqs = r.freqs;
+  a.rot = r.freqs != nullptr ? r.rot_dim : 0;
+  a.d = c.d;
+  a.magnitude = r.magnitude;
   a.sign = 1.f;
-  a.N = cache->tokens;
-  a.rows = cache->tokens;
-  a.cache = view_of(*cache);
-  return launch_rope<true>(a, interleaved != 0, cache->dtype, static_cast<cudaStream_t>(stream));
+  a.N = c.tokens;
+  a.rows = c.tokens;
+  a.cache = view_of(c);
+  return launch_rope<true>(a, r.interleaved != 0, c.dtype, static_cast<cudaStream_t>(stream));
 }
 
-size_t fa_paged_workspace_size(int tokens, int max_q, int Hq, int heads, int d) {
-  if (tokens < 0 || max_q < 0 || Hq < 0 || heads <= 0 || d < 0 || Hq % heads != 0)
+size_t fa_paged_workspace_size(int tokens, int max_q, int heads_q, int heads, int d) {
+  if (tokens < 0 || max_q < 0 || heads_q < 0 || heads <= 0 || d < 0 || heads_q % heads != 0)
     return static_cast<size_t>(-1);
-  if (tokens == 0 || max_q == 0 || Hq == 0) return 0;
-  return workspace_for(max_q, Hq / heads, d).bytes;
+  if (tokens == 0 || max_q == 0 || heads_q == 0) return 0;
+  return workspace_for(max_q < tokens ? max_q : tokens, heads_q / heads, d).bytes;
 }
 
-int fa_paged_attention(const fa_paged_cache* cache, const void* Q, const fa_strides* xq, void* O,
-                       const fa_strides* xo, float* L, int Hq, int max_q, int window_left,
-                       int window_right, float scale, void* workspace, size_t workspace_bytes,
-                       void* stream) {
-  const int st = check_cache(cache, true);
+int fa_paged_attention(const fa_paged_attention_args* args, void* stream) {
+  if (args == nullptr) return FA_ERR_INVALID;
+  const fa_paged_attention_args& r = *args;
+  const fa_paged_cache& c = r.cache;
+  const int st = check_cache(&c, true);
   if (st != FA_OK) return st;
-  if (Hq < 0 || Hq % cache->heads != 0 || max_q < 0) return FA_ERR_INVALID;
-  if (!(scale > 0.f) || !isfinite(scale)) return FA_ERR_INVALID;
-  if (Hq / cache->heads > 128) return FA_ERR_UNSUPPORTED;
-  if (cache->batch == 0 || cache->tokens == 0 || Hq == 0 || max_q == 0) return FA_OK;
-  if (!ok_ptr(Q) || !ok_ptr(O) || !ok_ptr(L, 4) || !ok_strides(xq) || !ok_strides(xo))
+  if (r.heads_q < 0 || r.heads_q % c.heads != 0 || r.max_q < 0) return FA_ERR_INVALID;
+  if (!(r.scale > 0.f) || !isfinite(r.scale)) return FA_ERR_INVALID;
+  const int group = r.heads_q / c.heads;
+  if (group > 128) return FA_ERR_UNSUPPORTED;
+  if (c.batch == 0 || c.tokens == 0 || r.heads_q == 0 || r.max_q == 0) return FA_OK;
+  if (!ok_ptr(r.q) || !ok_ptr(r.out) || !ok_ptr(r.lse, 4) || !ok_strides(r.qs) ||
+      !ok_strides(r.os))
     return FA_ERR_INVALID;
-  if (cache->num_pages == 0 || cache->table_width == 0) return FA_ERR_INVALID;
-  const int group = Hq / cache->heads;
-  if (!steps(xq->h, Hq) || !steps(xq->n, cache->tokens) || !steps(xo->h, Hq) ||
-      !steps(xo->n, cache->tokens) || !steps(cache->k_row, cache->page_size) ||
-      !steps(cache->k_head, cache->heads) || !steps(cache->k_page, cache->num_pages) ||
-      !steps(cache->v_row, cache->page_size) || !steps(cache->v_head, cache->heads) ||
-      !steps(cache->v_page, cache->num_pages))
+  if (c.num_pages == 0 || c.table_width == 0) return FA_ERR_INVALID;
+  if (!steps(r.qs.h, r.heads_q) || !steps(r.qs.n, c.tokens) || !steps(r.os.h, r.heads_q) ||
+      !steps(r.os.n, c.tokens) || !steps(c.k_row, c.page_size) || !steps(c.k_head, c.heads) ||
+      !steps(c.k_page, c.num_pages) || !steps(c.v_row, c.page_size) ||
+      !steps(c.v_head, c.heads) || !steps(c.v_page, c.num_pages))
     return FA_ERR_UNSUPPORTED;
-  const Workspace ws = workspace_for(max_q, group, cache->d);
-  if (!ok_ptr(workspace, 256) || workspace_bytes < ws.bytes) return FA_ERR_INVALID;
-  const AttentionArgs a{cache,
-                        Q,
-                        *xq,
-                        O,
-                        *xo,
-                        L,
+  const int max_q = r.max_q < c.tokens ? r.max_q : c.tokens;
+  const Workspace ws = workspace_for(max_q, group, c.d);
+  if (!ok_ptr(r.workspace, 256) || r.workspace_bytes < ws.bytes) return FA_ERR_INVALID;
+  const AttentionArgs a{&c,
+                        r.q,
+                        r.qs,
+                        r.out,
+                        r.os,
+                        r.lse,
                         group,
-                        max_q < cache->tokens ? max_q : cache->tokens,
-                        edge(window_left),
-                        edge(window_right),
-                        scale,
+                        max_q,
+                        edge(r.window_left),
+                        edge(r.window_right),
+                        r.scale,
                         ws,
-                        static_cast<uint8_t*>(workspace),
+                        static_cast<uint8_t*>(r.workspace),
                         static_cast<cudaStream_t>(stream)};
-  const bool bf = cache->dtype == FA_BF16;
-  if (cache->d == 64) return bf ? launch_attention<64, true>(a) : launch_attention<64, false>(a);
+  const bool bf = c.dtype == FA_BF16;
+  if (c.d == 64) return bf ? launch_attention<64, true>(a) : launch_attention<64, false>(a);
   return bf ? launch_attention<128, true>(a) : launch_attention<128, false>(a);
 }
 

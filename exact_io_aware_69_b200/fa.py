@@ -10,8 +10,10 @@ raises if the library is missing -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa.so")
@@ -68,36 +70,26 @@ SIGNATURES = {
 }
 
 
-class _Strides(ctypes.Structure):
-    """fa_strides: element strides of batch, head and row."""
-    _fields_ = [("b", ctypes.c_longlong), ("h", ctypes.c_longlong), ("n", ctypes.c_longlong)]
-
-
-class _PagedCache(ctypes.Structure):
-    """fa_paged_cache."""
-    _fields_ = ([(n, _vp) for n in ("k_pages", "v_pages")]
-                + [(n, ctypes.c_longlong) for n in ("k_page", "k_head", "k_row", "v_page",
-                                                    "v_head", "v_row")]
-                + [(n, _vp) for n in ("table", "cu_q", "seq_k")]
-                + [(n, _int) for n in ("table_row", "table_width", "num_pages", "page_size",
-                                       "heads", "d", "batch", "tokens", "dtype")])
-
-
 # Every symbol include/fa_paged.h declares, with its ctypes signature.
-_st, _pc = ctypes.POINTER(_Strides), ctypes.POINTER(_PagedCache)
 PAGED_SIGNATURES = {
-    "fa_rope": (_int, [_vp, _st, _vp, _st, _int] * 2 + [_vp, ctypes.c_longlong, _vp, _int, _f32]
-                + [_int] * 6 + [_vp]),
-    "fa_paged_append": (_int, [_pc, _vp, _st, _vp, _st, _vp, _st, _vp, _st, _int, _vp, _vp, _int,
-                               _f32, _int, _vp]),
+    "fa_rope": (_int, [ctypes.c_char_p, _vp]),
+    "fa_paged_append": (_int, [ctypes.c_char_p, _vp]),
     "fa_paged_workspace_size": (_sz, [_int] * 5),
-    "fa_paged_attention": (_int, [_pc, _vp, _st, _vp, _st, _vp, _int, _int, _int, _int, _f32, _vp,
-                                  _sz, _vp]),
+    "fa_paged_attention": (_int, [ctypes.c_char_p, _vp]),
     "fa_paged_device_status": (_int, [_vp]),
 }
+# Its argument structs as native struct formats: a call's arguments are packed into one
+# (building ctypes structures costs a few microseconds a call, as much as a small launch).
+_ROWS = "QQ6qi4x"                  # fa_rope_rows: x, y, xs, ys, heads
+_CACHE = "QQ6qQQQ9i4x"             # fa_paged_cache
+_ROPE_ARGS = struct.Struct("@" + 2 * _ROWS + "QqQ7if")
+_APPEND_ARGS = struct.Struct("@" + _CACHE + "QQ6q" + _ROWS + "QQ2if4x")
+_ATTENTION_ARGS = struct.Struct("@" + _CACHE + "QQQ6q4if4xQQ")
+_NO_ROWS = (0,) * 9
 
 _lib = None
 _paged_lib = None
+_torch = _raw_stream = None  # set with _paged_lib: a call's own import and lookup cost more
 
 
 class FaError(RuntimeError):
@@ -117,8 +109,13 @@ def load():
 
 def load_paged():
     """Load libfa_paged.so (raises if it has not been built)."""
-    global _paged_lib
+    global _paged_lib, _torch, _raw_stream
     if _paged_lib is None:
+        import torch
+        _torch = torch
+        # the current stream's handle without building a Stream object, where torch has it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
         _paged_lib = _load(PAGED_LIB_PATH, PAGED_SIGNATURES)
     return _paged_lib
 
@@ -364,115 +361,104 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, method: str = "none",
     return torch.tensor(freqs, dtype=torch.float64, device=device)
 
 
-def _strides_of(t, b, h, n, name):
-    """The fa_strides of dimensions b, h, n of t (None: absent) whose last one is dense."""
+def _bad(message):
+    return FaError(FA_ERR_INVALID, message)
+
+
+def _pack(fields, *values):
+    try:
+        return fields.pack(*values)
+    except (struct.error, OverflowError) as e:  # a number that its C type does not hold
+        raise _bad(str(e)) from None
+
+
+def _on_stream(stream, call, *args):
+    """call(*args) with `stream` (and its device) as the current one, so that what the call
+    allocates belongs to it."""
+    import torch
+    with torch.cuda.stream(stream):
+        return call(*args)
+
+
+def _place(t, name):
+    """The device index of a CUDA tensor."""
+    device = t.get_device()
+    if device < 0:
+        raise _bad(f"{name} is not a CUDA tensor")
+    return device
+
+
+def _strides3(t, b, h, n, name):
+    """Element strides of dimensions b, h, n of t (-1: absent), whose last is dense."""
     st, shape = t.stride(), t.shape
     if st[-1] != 1 and shape[-1] != 1:
-        raise FaError(FA_ERR_INVALID, f"{name}: the last dimension is not dense")
+        raise _bad(f"{name}: the last dimension is not dense")
     # a dimension of one row is never stepped over
-    return _Strides(*(0 if i is None or shape[i] == 1 else st[i] for i in (b, h, n)))
+    return (st[b] if b >= 0 and shape[b] != 1 else 0, st[h] if shape[h] != 1 else 0,
+            st[n] if shape[n] != 1 else 0)
 
 
-def _same(t, name, like, dtype=None):
-    """t lies on like's device and has its (or the given) dtype."""
-    if t.get_device() != like.get_device() or not t.is_cuda:
-        raise FaError(FA_ERR_INVALID, f"{name} is not on the device of the others")
-    if t.dtype != (like.dtype if dtype is None else dtype):
-        raise FaError(FA_ERR_INVALID, f"{name} has dtype {t.dtype}")
+def _rope_rows(x, y, name, device, dtype, b, h, n):
+    """(y, the fields of fa_rope_rows) of rows rotated from x into y (None: allocated)."""
+    if x.get_device() != device or x.dtype != dtype:
+        raise _bad(f"{name}: not on the device or of the dtype of the others")
+    xs = _strides3(x, b, h, n, name)
+    if y is None:
+        y = _torch.empty_like(x)
+        ys = xs if y.stride() == x.stride() else _strides3(y, b, h, n, name)
+    else:
+        if y.get_device() != device or y.dtype != dtype or y.shape != x.shape:
+            raise _bad(f"{name}_out: not of {name}'s device, dtype or shape")
+        ys = _strides3(y, b, h, n, name + "_out")
+        if 0 in ys and any(s == 0 and y.shape[i] > 1 for s, i in zip(ys, (b, h, n)) if i >= 0):
+            raise _bad(f"{name}_out: rows share memory")
+    return y, (x.data_ptr(), y.data_ptr(), *xs, *ys, x.shape[h])
 
 
-def _check_freqs(freqs, like):
-    import torch
-    _same(freqs, "freqs", like, torch.float64)
-    if freqs.dim() != 1 or not freqs.is_contiguous():
-        raise FaError(FA_ERR_INVALID, "freqs is not a dense vector")
+def _check_freqs(freqs, device):
+    if freqs.get_device() != device or freqs.dtype != _torch.float64 or freqs.dim() != 1 or \
+            not freqs.is_contiguous():
+        raise _bad("freqs is not a dense float64 vector on the device of the others")
     return 2 * freqs.shape[0]
 
 
-class _Launch:
-    """The device and stream of a call: the tensors' device becomes the current one, and
-    tensors allocated for the call are kept for a stream that is not the current one."""
-
-    __slots__ = ("device", "before", "stream", "other")
-
-    def __init__(self, like, stream):
-        self.device, self.stream, self.before = like.get_device(), stream, None
-
-    def __enter__(self):
-        import torch
-        cuda = torch.cuda
-        now = cuda.current_device()
-        if now != self.device:
-            self.before = now
-            cuda.set_device(self.device)
-        current = cuda.current_stream()
-        self.other = self.stream is not None and self.stream != current
-        if self.stream is None:
-            self.stream = current
-        elif self.stream.device_index != self.device:
-            self.__exit__()
-            raise FaError(FA_ERR_INVALID, "the stream is of another device than the tensors")
-        return self
-
-    def keep(self, *tensors):
-        if self.other:
-            for t in tensors:
-                t.record_stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            import torch
-            torch.cuda.set_device(self.before)
-            self.before = None
-
-
 def _rope(q, k, freqs, positions, magnitude, interleaved, layout, q_out, k_out, stream, inverse):
-    import torch
-    lib = load_paged()
-    dtype = _dtype_code(q)
-    if not q.is_cuda:
-        raise FaError(FA_ERR_INVALID, "q is not a CUDA tensor")
+    if stream is not None:
+        return _on_stream(stream, _rope, q, k, freqs, positions, magnitude, interleaved, layout,
+                          q_out, k_out, None, inverse)
+    lib = _paged_lib or load_paged()
+    torch = _torch
+    dtype = q.dtype
+    code = _dtype_code(q)
+    device = _place(q, "q")
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _rope(q, k, freqs, positions, magnitude, interleaved, layout, q_out, k_out,
+                         None, inverse)
     B, H, N, d = _dims(q, layout)
     h, n = (1, 2) if layout == "bhnd" else (2, 1)
-    rot = _check_freqs(freqs, q)
-    Hk = 0
+    rot = _check_freqs(freqs, device)
+    q_out, q_rows = _rope_rows(q, q_out, "q", device, dtype, 0, h, n)
+    k_rows = _NO_ROWS
     if k is not None:
-        _same(k, "k", q)
-        Bk, Hk, Nk, dk = _dims(k, layout)
-        if (Bk, Nk, dk) != (B, N, d):
-            raise FaError(FA_ERR_INVALID, "k batch, length or head dim differ from q")
-    pos_row = 0
+        if k.dim() != 4 or k.shape[0] != B or k.shape[n] != N or k.shape[3] != d:
+            raise _bad("k batch, length or head dim differ from q")
+        k_out, k_rows = _rope_rows(k, k_out, "k", device, dtype, 0, h, n)
+    else:
+        k_out = None
+    where = pos_row = 0
     if positions is not None:
-        _same(positions, "positions", q, torch.int32)
-        if positions.shape == (B, N) and (N <= 1 or positions.stride(1) == 1):
-            pos_row = positions.stride(0) if B > 1 else 0
-        elif positions.shape != (N,) or (N > 1 and positions.stride(0) != 1):
-            raise FaError(FA_ERR_INVALID, "positions is not a dense [N] or [B, N] tensor")
-    with _Launch(q, stream) as at:
-        outs = []
-        for x, y, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-            if x is None:
-                outs.append(None)
-                continue
-            if y is None:
-                y = torch.empty(x.shape, device=x.device, dtype=x.dtype)
-                at.keep(y)
-            else:
-                _same(y, name, x)
-                if y.shape != x.shape:
-                    raise FaError(FA_ERR_INVALID, f"{name} has another shape")
-            outs.append(y)
-        q_out, k_out = outs
-        args = [q.data_ptr(), _strides_of(q, 0, h, n, "q"), q_out.data_ptr(),
-                _strides_of(q_out, 0, h, n, "q_out"), H]
-        if k is None:
-            args += [None, None, None, None, 0]
-        else:
-            args += [k.data_ptr(), _strides_of(k, 0, h, n, "k"), k_out.data_ptr(),
-                     _strides_of(k_out, 0, h, n, "k_out"), Hk]
-        rc = lib.fa_rope(*args, _ptr_or_none(positions), pos_row, freqs.data_ptr(), rot,
-                         magnitude, 1 if interleaved else 0, inverse, B, N, d, dtype,
-                         at.stream.cuda_stream)
+        where = positions.data_ptr()
+        if positions.get_device() != device or positions.dtype != torch.int32:
+            raise _bad("positions is not an int32 tensor on the device of the others")
+        st = positions.stride()
+        if positions.shape == (B, N) and (N <= 1 or st[1] == 1):
+            pos_row = st[0] if B > 1 else 0
+        elif positions.shape != (N,) or (N > 1 and st[0] != 1):
+            raise _bad("positions is not a dense [N] or [B, N] tensor")
+    rc = lib.fa_rope(_pack(_ROPE_ARGS, *q_rows, *k_rows, where, pos_row, freqs.data_ptr(), rot,
+                           1 if interleaved else 0, inverse, B, N, d, code, magnitude),
+                     _raw_stream(device))
     if rc != FA_OK:
         raise FaError(rc, "fa_rope")
     return q_out, k_out
@@ -497,37 +483,36 @@ def rope_backward(dq, dk, freqs, positions=None, magnitude: float = 1.0,
                  1)
 
 
-def _paged_cache(x, name, k_pages, v_pages, page_table, cu_q, seq_k, page_layout):
-    """The fa_paged_cache of these tensors for the packed rows x [T, H, d]."""
-    import torch
-    dtype = _dtype_code(x)
-    if not x.is_cuda or x.dim() != 3:
-        raise FaError(FA_ERR_INVALID, f"{name} is not a packed [T, H, d] CUDA tensor")
-    _same(k_pages, "k_pages", x)
-    _same(v_pages, "v_pages", x)
-    i32 = torch.int32
-    _same(page_table, "page_table", x, i32)
-    _same(cu_q, "cu_q", x, i32)
-    _same(seq_k, "seq_k", x, i32)
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
-        raise FaError(FA_ERR_INVALID, "k_pages and v_pages are not 4-D tensors of one shape")
+def _paged_cache(x, name, device, k_pages, v_pages, page_table, cu_q, seq_k, page_layout):
+    """The fields of the fa_paged_cache of these tensors for the packed rows x [T, H, d]."""
+    code = _dtype_code(x)
+    dtype, i32 = x.dtype, _torch.int32
+    if x.dim() != 3:
+        raise _bad(f"{name} is not a packed [T, H, d] tensor")
+    if k_pages.get_device() != device or v_pages.get_device() != device or \
+            k_pages.dtype != dtype or v_pages.dtype != dtype:
+        raise _bad(f"k_pages or v_pages: not of {name}'s device or dtype")
+    if page_table.get_device() != device or cu_q.get_device() != device or \
+            seq_k.get_device() != device or page_table.dtype != i32 or cu_q.dtype != i32 or \
+            seq_k.dtype != i32:
+        raise _bad(f"page_table, cu_q or seq_k: not int32 tensors on {name}'s device")
     if page_layout not in LAYOUTS:
-        raise FaError(FA_ERR_INVALID, f"layout {page_layout!r}")
+        raise _bad(f"layout {page_layout!r}")
     h, n = (1, 2) if page_layout == "bhnd" else (2, 1)
-    shape = k_pages.shape
+    shape, table = k_pages.shape, page_table.shape
+    if len(shape) != 4 or v_pages.shape != shape:
+        raise _bad("k_pages and v_pages are not 4-D tensors of one shape")
     batch = seq_k.shape[0] if seq_k.dim() == 1 else -1
-    if page_table.dim() != 2 or page_table.shape[0] != batch or cu_q.shape != (batch + 1,) or \
+    if len(table) != 2 or table[0] != batch or cu_q.shape != (batch + 1,) or \
             shape[3] != x.shape[2]:
-        raise FaError(FA_ERR_INVALID, "page_table, cu_q, seq_k or the head dims do not fit")
-    width = page_table.shape[1]
-    if not (cu_q.is_contiguous() and seq_k.is_contiguous()) or \
-            (width > 1 and page_table.stride(1) != 1):
-        raise FaError(FA_ERR_INVALID, "page_table, cu_q or seq_k is not dense")
-    ks, vs = _strides_of(k_pages, 0, h, n, "k_pages"), _strides_of(v_pages, 0, h, n, "v_pages")
-    return _PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), ks.b, ks.h, ks.n, vs.b, vs.h, vs.n,
-                       page_table.data_ptr(), cu_q.data_ptr(), seq_k.data_ptr(),
-                       page_table.stride(0) if batch > 1 else 0, width, shape[0], shape[n],
-                       shape[h], shape[3], batch, x.shape[0], dtype)
+        raise _bad("page_table, cu_q, seq_k or the head dims do not fit")
+    st = page_table.stride()
+    if not (cu_q.is_contiguous() and seq_k.is_contiguous()) or (table[1] > 1 and st[1] != 1):
+        raise _bad("page_table, cu_q or seq_k is not dense")
+    return (k_pages.data_ptr(), v_pages.data_ptr(), *_strides3(k_pages, 0, h, n, "k_pages"),
+            *_strides3(v_pages, 0, h, n, "v_pages"), page_table.data_ptr(), cu_q.data_ptr(),
+            seq_k.data_ptr(), st[0] if batch > 1 else 0, table[1], shape[0], shape[n], shape[h],
+            shape[3], batch, x.shape[0], code)
 
 
 def paged_append(k, v, k_pages, v_pages, page_table, cu_q, seq_k, q=None, freqs=None,
@@ -542,44 +527,45 @@ def paged_append(k, v, k_pages, v_pages, page_table, cu_q, seq_k, q=None, freqs=
     page_table, cu_q and seq_k are int32 CUDA tensors. With `freqs` the keys are rotated on
     the way as in rope(), each at its position in the sequence (or at positions [T]), and so
     is q [T, Hq, d], if given; returns the rotated q (q_out, which may be q), or None."""
-    import torch
-    lib = load_paged()
-    cache = _paged_cache(k, "k", k_pages, v_pages, page_table, cu_q, seq_k, page_layout)
-    _same(v, "v", k)
+    if stream is not None:
+        return _on_stream(stream, paged_append, k, v, k_pages, v_pages, page_table, cu_q, seq_k, q,
+                          freqs, magnitude, interleaved, positions, q_out, page_layout)
+    lib = _paged_lib or load_paged()
+    torch = _torch
+    device = _place(k, "k")
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return paged_append(k, v, k_pages, v_pages, page_table, cu_q, seq_k, q, freqs,
+                                magnitude, interleaved, positions, q_out, page_layout)
+    cache = _paged_cache(k, "k", device, k_pages, v_pages, page_table, cu_q, seq_k, page_layout)
     T, heads, d = k.shape
-    if v.shape != k.shape or heads != cache.heads:
-        raise FaError(FA_ERR_INVALID, "k, v and the cache have different shapes or heads")
-    rot = 0 if freqs is None else _check_freqs(freqs, k)
+    if v.get_device() != device or v.dtype != k.dtype or v.shape != k.shape or heads != cache[15]:
+        raise _bad("k, v and the cache have different devices, dtypes, shapes or heads")
+    rot = 0 if freqs is None else _check_freqs(freqs, device)
+    where = 0
     if positions is not None:
-        _same(positions, "positions", k, torch.int32)
-        if positions.shape != (T,) or not positions.is_contiguous():
-            raise FaError(FA_ERR_INVALID, "positions is not a dense [T] tensor")
-    if q is not None and freqs is None:
-        raise FaError(FA_ERR_INVALID, "q without freqs: there is nothing to do to it")
-    with _Launch(k, stream) as at:
-        args = [None, None, None, None, 0]
-        if q is not None:
-            _same(q, "q", k)
-            if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d:
-                raise FaError(FA_ERR_INVALID, "q is not [T, Hq, d]")
-            if q_out is None:
-                q_out = torch.empty(q.shape, device=q.device, dtype=q.dtype)
-                at.keep(q_out)
-            else:
-                _same(q_out, "q_out", q)
-                if q_out.shape != q.shape:
-                    raise FaError(FA_ERR_INVALID, "q_out has another shape")
-            args = [q.data_ptr(), _strides_of(q, None, 1, 0, "q"), q_out.data_ptr(),
-                    _strides_of(q_out, None, 1, 0, "q_out"), q.shape[1]]
-        rc = lib.fa_paged_append(cache, k.data_ptr(), _strides_of(k, None, 1, 0, "k"),
-                                 v.data_ptr(), _strides_of(v, None, 1, 0, "v"), *args,
-                                 _ptr_or_none(positions), _ptr_or_none(freqs), rot, magnitude,
-                                 1 if interleaved else 0, at.stream.cuda_stream)
+        where = positions.data_ptr()
+        if positions.get_device() != device or positions.dtype != torch.int32 or \
+                positions.shape != (T,) or not positions.is_contiguous():
+            raise _bad("positions is not a dense int32 [T] tensor on the device of the others")
+    rows = _NO_ROWS
+    if q is not None:
+        if freqs is None:
+            raise _bad("q without freqs: there is nothing to do to it")
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d:
+            raise _bad("q is not [T, Hq, d]")
+        q_out, rows = _rope_rows(q, q_out, "q", device, k.dtype, -1, 1, 0)
+    rc = lib.fa_paged_append(
+        _pack(_APPEND_ARGS, *cache, k.data_ptr(), v.data_ptr(), *_strides3(k, -1, 1, 0, "k"),
+              *_strides3(v, -1, 1, 0, "v"), *rows, where,
+              0 if freqs is None else freqs.data_ptr(), rot, 1 if interleaved else 0, magnitude),
+        _raw_stream(device))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_append")
     return None if q is None else q_out
 
 
+@functools.lru_cache(maxsize=256)
 def paged_workspace_size(tokens: int, max_q: int, heads_q: int, heads: int, d: int) -> int:
     """Bytes of workspace of paged_attention() for these sizes (whatever the lengths)."""
     return int(load_paged().fa_paged_workspace_size(tokens, max_q, heads_q, heads, d))
@@ -594,43 +580,49 @@ def paged_attention(q, k_pages, v_pages, page_table, cu_q, seq_k, max_q: int | N
     h // (Hq // Hkv). The mask is forward()'s, bottom-right aligned over each sequence's
     seq_k keys; here `causal` is the default. max_q: the most new tokens that any sequence
     has (None: T); 1 for a decode step. Rows behind the last sequence are not written."""
-    import torch
-    lib = load_paged()
-    cache = _paged_cache(q, "q", k_pages, v_pages, page_table, cu_q, seq_k, page_layout)
+    if stream is not None:
+        return _on_stream(stream, paged_attention, q, k_pages, v_pages, page_table, cu_q, seq_k,
+                          max_q, causal, scale, window, page_layout, out, lse, workspace)
+    lib = _paged_lib or load_paged()
+    torch = _torch
+    device = _place(q, "q")
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return paged_attention(q, k_pages, v_pages, page_table, cu_q, seq_k, max_q, causal,
+                                   scale, window, page_layout, out, lse, workspace)
+    cache = _paged_cache(q, "q", device, k_pages, v_pages, page_table, cu_q, seq_k, page_layout)
     T, H, d = q.shape
     wl, wr = _window(causal, window)
     if max_q is None:
         max_q = T
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _Launch(q, stream) as at:
-        if out is None:
-            out = torch.empty(q.shape, device=q.device, dtype=q.dtype)
-            at.keep(out)
-        else:
-            _same(out, "out", q)
-            if out.shape != q.shape:
-                raise FaError(FA_ERR_INVALID, "out has another shape")
-        if lse is None:
-            lse = torch.empty((H, T), device=q.device, dtype=torch.float32)
-            at.keep(lse)
-        else:
-            _same(lse, "lse", q, torch.float32)
-            if lse.shape != (H, T) or not lse.is_contiguous():
-                raise FaError(FA_ERR_INVALID, "lse is not a dense [Hq, T] tensor")
-        need = lib.fa_paged_workspace_size(T, max_q, H, cache.heads, d)
-        ws = None
-        if workspace is not None:
-            _same(workspace, "workspace", q, workspace.dtype)
-            ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        elif 0 < need < 1 << 62:
-            workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-            at.keep(workspace)
-            ws = workspace.data_ptr()
-        rc = lib.fa_paged_attention(cache, q.data_ptr(), _strides_of(q, None, 1, 0, "q"),
-                                    out.data_ptr(), _strides_of(out, None, 1, 0, "out"),
-                                    lse.data_ptr(), H, max_q, wl, wr, scale, ws, need,
-                                    at.stream.cuda_stream)
+    qs = _strides3(q, -1, 1, 0, "q")
+    if out is None:
+        out = torch.empty_like(q)
+        os_ = qs if out.stride() == q.stride() else _strides3(out, -1, 1, 0, "out")
+    else:
+        if out.get_device() != device or out.dtype != q.dtype or out.shape != q.shape:
+            raise _bad("out: not of q's device, dtype or shape")
+        os_ = _strides3(out, -1, 1, 0, "out")
+    if lse is None:
+        lse = torch.empty((H, T), device=q.device, dtype=torch.float32)
+    elif lse.get_device() != device or lse.dtype != torch.float32 or lse.shape != (H, T) or \
+            not lse.is_contiguous():
+        raise _bad("lse is not a dense float32 [Hq, T] tensor on q's device")
+    need = paged_workspace_size(T, max_q, H, cache[15], d)
+    ws = 0
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise _bad("workspace is not a dense tensor on q's device")
+        ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif 0 < need < 1 << 62:
+        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        ws = workspace.data_ptr()
+    rc = lib.fa_paged_attention(
+        _pack(_ATTENTION_ARGS, *cache, q.data_ptr(), out.data_ptr(), lse.data_ptr(), *qs, *os_, H,
+              max_q, wl, wr, scale, ws, need),
+        _raw_stream(device))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_attention")
     return out, lse

@@ -63,50 +63,83 @@ typedef struct {
     int table_row, table_width;
     int num_pages, page_size;          /* page_size: a power of two, 16 .. 1024 */
     int heads, d;                      /* key heads; d = 64 or 128 (append: see there) */
-    int batch, tokens;                 /* sequences; packed rows that Q, K, V, O have */
+    int batch, tokens;                 /* sequences (up to 8192); packed rows of Q, K, V, O */
     int dtype;                         /* FA_BF16 or FA_FP16 */
+    int reserved;
 } fa_paged_cache;
 
-/*
- * Rotates Q [B][Hq][N][d] and, with Hk > 0, K [B][Hk][N][d] in one launch; `inverse` = 1
- * turns by -a instead, which is the gradient of the rotation (same magnitude). Row n of
- * batch b is at positions[b * pos_row + n] (pos_row = 0: the same for every batch), or at
- * n when positions is NULL. Y may be X with the same strides (in place); otherwise they
- * must not overlap. d and rot_dim are multiples of 16, 16 <= rot_dim <= d <= 1024.
- */
-int fa_rope(const void *Xq, const fa_strides *xq, void *Yq, const fa_strides *yq, int Hq,
-            const void *Xk, const fa_strides *xk, void *Yk, const fa_strides *yk, int Hk,
-            const int *positions, long long pos_row, const double *freqs, int rot_dim,
-            float magnitude, int interleaved, int inverse, int B, int N, int d, int dtype,
-            void *stream);
+/* Rows of heads that are rotated from x to y; heads = 0: none, the rest is not looked at. */
+typedef struct {
+    const void *x;
+    void *y;
+    fa_strides xs, ys;
+    int heads;
+    int reserved;
+} fa_rope_rows;
 
 /*
- * Writes the new tokens' keys and values, K and V [tokens][heads][d] (strides h and n of
- * xk, xv), into their pages: V as it is, K rotated (freqs not NULL) or as it is (freqs
- * NULL). Token i of a sequence takes position seq_k[b] - n + i; `positions` [tokens], if
- * given, replaces it in the rotation only. With Hq > 0 it also rotates Q [tokens][Hq][d]
- * into Yq (which may be Xq) in the same launch; that needs freqs. Here d is any multiple
- * of 16 up to 1024. Tokens of sequences that share a page row race for it.
+ * Rotates q [batch][q.heads][rows][d] and k [batch][k.heads][rows][d] in one launch;
+ * `inverse` = 1 turns by -a instead, which is the gradient of the rotation (same
+ * magnitude). Row n of batch b is at positions[b * pos_row + n] (pos_row = 0: the same for
+ * every batch), or at n when positions is NULL. y may be x with the same strides (in
+ * place); otherwise they must not overlap. d and rot_dim are multiples of 16,
+ * 16 <= rot_dim <= d <= 1024.
  */
-int fa_paged_append(const fa_paged_cache *cache, const void *K, const fa_strides *xk,
-                    const void *V, const fa_strides *xv, const void *Xq, const fa_strides *xq,
-                    void *Yq, const fa_strides *yq, int Hq, const int *positions,
-                    const double *freqs, int rot_dim, float magnitude, int interleaved,
-                    void *stream);
+typedef struct {
+    fa_rope_rows q, k;
+    const int *positions;
+    long long pos_row;
+    const double *freqs;               /* [rot_dim / 2] */
+    int rot_dim, interleaved, inverse;
+    int batch, rows, d, dtype;
+    float magnitude;
+} fa_rope_args;
+int fa_rope(const fa_rope_args *args, void *stream);
 
 /*
- * Exact attention of the packed queries Q [tokens][Hq][d] (strides h and n of xq) over
- * the cache: O [tokens][Hq][d] and L [Hq][tokens] (fp32, natural log). Hq is a multiple of
- * cache->heads, Hq / heads <= 128. max_q bounds the new tokens of any sequence (one with
- * more is left out, as above); it picks the kernel. Work is shared out evenly over the
- * SMs by key tiles, so a sequence's keys may be split between CTAs; the parts are joined
- * by their log-sum-exps in a fixed order, and results are the same on every call.
+ * Writes the new tokens' keys and values, k and v [tokens][heads][d] (strides h and n),
+ * into their pages: V as it is, K rotated (freqs not NULL) or as it is (freqs NULL). Token
+ * i of a sequence takes position seq_k[b] - n + i; `positions` [tokens], if given, replaces
+ * it in the rotation only. With q.heads > 0 it also rotates q [tokens][q.heads][d] (strides
+ * h and n) in the same launch; that needs freqs. Here d is any multiple of 16 up to 1024.
+ * Tokens of sequences that share a page row race for it.
  */
-size_t fa_paged_workspace_size(int tokens, int max_q, int Hq, int heads, int d);
-int fa_paged_attention(const fa_paged_cache *cache, const void *Q, const fa_strides *xq, void *O,
-                       const fa_strides *xo, float *L, int Hq, int max_q, int window_left,
-                       int window_right, float scale, void *workspace, size_t workspace_bytes,
-                       void *stream);
+typedef struct {
+    fa_paged_cache cache;
+    const void *k, *v;
+    fa_strides ks, vs;
+    fa_rope_rows q;
+    const int *positions;
+    const double *freqs;
+    int rot_dim, interleaved;
+    float magnitude;
+    int reserved;
+} fa_paged_append_args;
+int fa_paged_append(const fa_paged_append_args *args, void *stream);
+
+/*
+ * Exact attention of the packed queries q [tokens][heads_q][d] (strides h and n) over the
+ * cache: out [tokens][heads_q][d] and lse [heads_q][tokens] (fp32, natural log). heads_q is
+ * a multiple of cache.heads, heads_q / cache.heads <= 128. max_q bounds the new tokens of
+ * any sequence (one with more is left out, as above); it picks the kernel. Work is shared
+ * out evenly over the SMs by key tiles, so a sequence's keys may be split between CTAs; the
+ * parts are joined by their log-sum-exps in a fixed order, and results are the same on
+ * every call. The workspace is 256-byte aligned; its contents do not matter.
+ */
+typedef struct {
+    fa_paged_cache cache;
+    const void *q;
+    void *out;
+    float *lse;
+    fa_strides qs, os;
+    int heads_q, max_q, window_left, window_right;
+    float scale;
+    int reserved;
+    void *workspace;
+    size_t workspace_bytes;
+} fa_paged_attention_args;
+size_t fa_paged_workspace_size(int tokens, int max_q, int heads_q, int heads, int d);
+int fa_paged_attention(const fa_paged_attention_args *args, void *stream);
 
 /* fa_get_device_status for the kernels of this library: synchronises `stream`, returns
  * and clears the current device's error word (FA_ERR_INVALID: see above). */

@@ -29,7 +29,7 @@ def test_every_declared_function_is_exported_and_bound(lib):
 
 
 def strides(b=4096, h=128, n=1024):
-    return ctypes.byref(fa._Strides(b, h, n))
+    return b, h, n
 
 
 def cache(**kw):
@@ -37,17 +37,43 @@ def cache(**kw):
              v_page=16 * 256, v_head=128, v_row=256, table=P + 0x200000, cu_q=P + 0x300000,
              seq_k=P + 0x400000, table_row=8, table_width=8, num_pages=100, page_size=16, heads=2,
              d=128, batch=3, tokens=5, dtype=fa.FA_BF16)
+    assert set(kw) <= set(c)
     c.update(kw)
-    return fa._PagedCache(**c)
+    return [v or 0 for v in c.values()]
+
+
+def pack(fields, values, defaults):
+    assert set(values) <= set(defaults)
+    flat = []
+    for v in {**defaults, **values}.values():
+        flat += list(v) if isinstance(v, (tuple, list)) else [v or 0]
+    return fields.pack(*flat)
 
 
 def rope(lib, **kw):
-    a = dict(xq=P, sq=strides(), yq=P + 0x100000, syq=strides(), hq=4, xk=P + 0x200000,
-             sk=strides(), yk=P + 0x300000, syk=strides(), hk=2, pos=P + 0x400000, row=64,
-             freqs=P + 0x500000, rot=64, mag=1.0, il=0, inv=0, B=2, N=64, d=128,
-             dtype=fa.FA_BF16, stream=None)
-    a.update(kw)
-    return lib.fa_rope(*a.values())
+    return lib.fa_rope(pack(fa._ROPE_ARGS, kw, dict(
+        xq=P, yq=P + 0x100000, sq=strides(), syq=strides(), hq=4, xk=P + 0x200000,
+        yk=P + 0x300000, sk=strides(), syk=strides(), hk=2, pos=P + 0x400000, row=64,
+        freqs=P + 0x500000, rot=64, il=0, inv=0, B=2, N=64, d=128, dtype=fa.FA_BF16,
+        mag=1.0)), None)
+
+
+def test_the_bindings_structs_are_the_headers(tmp_path):
+    """Sizes and the offset of a late field of each argument struct, from the C compiler."""
+    import subprocess
+    source = tmp_path / "sizes.c"
+    source.write_text('#include "fa_paged.h"\n#include <stddef.h>\n#include <stdio.h>\n'
+                      'int main(void) { printf("%zu %zu %zu %zu %zu %zu", sizeof(fa_rope_args), '
+                      'sizeof(fa_paged_append_args), sizeof(fa_paged_attention_args), '
+                      'offsetof(fa_rope_args, magnitude), offsetof(fa_paged_append_args, '
+                      'magnitude), offsetof(fa_paged_attention_args, workspace_bytes)); }')
+    subprocess.run(["gcc", "-I", build.INCLUDE, str(source), "-o", str(tmp_path / "sizes")],
+                   check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "sizes")], capture_output=True,
+                                          check=True).stdout.split()]
+    assert got == [fa._ROPE_ARGS.size, fa._APPEND_ARGS.size, fa._ATTENTION_ARGS.size,
+                   fa._ROPE_ARGS.size - 4, fa._APPEND_ARGS.size - 8,
+                   fa._ATTENTION_ARGS.size - 8]
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -55,7 +81,7 @@ def rope(lib, **kw):
     (dict(hq=-1), fa.FA_ERR_INVALID), (dict(d=0), fa.FA_ERR_INVALID),
     (dict(xq=None), fa.FA_ERR_INVALID), (dict(yq=P + 8), fa.FA_ERR_INVALID),
     (dict(xk=P + 2), fa.FA_ERR_INVALID), (dict(yk=None), fa.FA_ERR_INVALID),
-    (dict(sq=None), fa.FA_ERR_INVALID), (dict(sk=strides(n=4)), fa.FA_ERR_INVALID),
+    (dict(sk=strides(n=4)), fa.FA_ERR_INVALID),
     (dict(syq=strides(h=-8)), fa.FA_ERR_INVALID), (dict(pos=P + 2), fa.FA_ERR_INVALID),
     (dict(row=-1), fa.FA_ERR_INVALID), (dict(freqs=None), fa.FA_ERR_INVALID),
     (dict(freqs=P + 4), fa.FA_ERR_INVALID), (dict(rot=144), fa.FA_ERR_INVALID),
@@ -83,11 +109,10 @@ BAD_CACHE = [
 
 
 def append(lib, c, **kw):
-    a = dict(k=P + 0x500000, sk=strides(), v=P + 0x600000, sv=strides(), xq=P + 0x700000,
-             sq=strides(), yq=P + 0x800000, syq=strides(), hq=4, pos=None, freqs=P + 0x900000,
-             rot=64, mag=1.0, il=0, stream=None)
-    a.update(kw)
-    return lib.fa_paged_append(ctypes.byref(c), *a.values())
+    return lib.fa_paged_append(pack(fa._APPEND_ARGS, kw, dict(
+        cache=c, k=P + 0x500000, v=P + 0x600000, sk=strides(), sv=strides(), xq=P + 0x700000,
+        yq=P + 0x800000, sq=strides(), syq=strides(), hq=4, pos=0, freqs=P + 0x900000, rot=64,
+        il=0, mag=1.0)), None)
 
 
 @pytest.mark.parametrize("kw,code", BAD_CACHE + [
@@ -98,7 +123,7 @@ def test_append_rejects_a_bad_cache(lib, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(k=None), fa.FA_ERR_INVALID), (dict(v=P + 4), fa.FA_ERR_INVALID),
-    (dict(sk=None), fa.FA_ERR_INVALID), (dict(sv=strides(h=12)), fa.FA_ERR_INVALID),
+    (dict(sv=strides(h=12)), fa.FA_ERR_INVALID),
     (dict(hq=-1), fa.FA_ERR_INVALID), (dict(freqs=None), fa.FA_ERR_INVALID),
     (dict(yq=None), fa.FA_ERR_INVALID), (dict(rot=200), fa.FA_ERR_INVALID),
     (dict(rot=40), fa.FA_ERR_UNSUPPORTED), (dict(pos=P + 1), fa.FA_ERR_INVALID),
@@ -109,10 +134,9 @@ def test_append_rejects_before_launch(lib, kw, code):
 
 
 def attention(lib, c, **kw):
-    a = dict(q=P + 0x500000, sq=strides(), o=P + 0x600000, so=strides(), L=P + 0x700000, hq=8,
-             max_q=2, wl=-1, wr=0, scale=0.1, ws=P + 0x800000, ws_bytes=1 << 40, stream=None)
-    a.update(kw)
-    return lib.fa_paged_attention(ctypes.byref(c), *a.values())
+    return lib.fa_paged_attention(pack(fa._ATTENTION_ARGS, kw, dict(
+        cache=c, q=P + 0x500000, o=P + 0x600000, L=P + 0x700000, sq=strides(), so=strides(), hq=8,
+        max_q=2, wl=-1, wr=0, scale=0.1, ws=P + 0x800000, ws_bytes=1 << 40)), None)
 
 
 @pytest.mark.parametrize("kw,code", BAD_CACHE + [(dict(d=80), fa.FA_ERR_UNSUPPORTED)])
@@ -123,7 +147,9 @@ def test_attention_rejects_a_bad_cache(lib, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), fa.FA_ERR_INVALID), (dict(o=P + 8), fa.FA_ERR_INVALID),
     (dict(L=None), fa.FA_ERR_INVALID), (dict(sq=strides(n=12)), fa.FA_ERR_INVALID),
-    (dict(so=None), fa.FA_ERR_INVALID), (dict(hq=7), fa.FA_ERR_INVALID),
+    (dict(sq=strides(h=0)), fa.FA_ERR_UNSUPPORTED), (dict(ws=None), fa.FA_ERR_INVALID),
+    (dict(ws=P + 0x800010), fa.FA_ERR_INVALID), (dict(ws_bytes=1000), fa.FA_ERR_INVALID),
+    (dict(hq=7), fa.FA_ERR_INVALID),
     (dict(max_q=-1), fa.FA_ERR_INVALID), (dict(scale=0.0), fa.FA_ERR_INVALID),
     (dict(scale=float("nan")), fa.FA_ERR_INVALID), (dict(hq=2 * 129), fa.FA_ERR_UNSUPPORTED),
     (dict(hq=0), fa.FA_OK),
@@ -132,7 +158,20 @@ def test_attention_rejects_before_launch(lib, kw, code):
     assert attention(lib, cache(), **kw) == code
 
 
-def test_workspace_size_refuses(lib):
+def test_null_arguments(lib):
+    for name in ("fa_rope", "fa_paged_append", "fa_paged_attention"):
+        assert getattr(lib, name)(None, None) == fa.FA_ERR_INVALID
+
+
+def test_workspace_size(lib):
+    """Two parts per CTA (148) of 16, 32, 64 or 256 rows, d outputs and a log-sum-exp each,
+    behind 32 bytes per CTA."""
+    for max_q, hq, heads, d, rows in ((1, 8, 8, 64, 16), (4, 32, 8, 128, 16), (5, 32, 8, 64, 32),
+                                      (64, 2, 2, 128, 64), (65, 2, 2, 128, 256)):
+        assert lib.fa_paged_workspace_size(1000, max_q, hq, heads, d) == \
+            148 * 32 + 2 * 148 * rows * (d + 1) * 4
+    assert lib.fa_paged_workspace_size(0, 1, 8, 2, 128) == 0
+    assert lib.fa_paged_workspace_size(7, 2, 7, 2, 128) == ctypes.c_size_t(-1).value
     assert lib.fa_paged_workspace_size(-1, 1, 8, 2, 128) == ctypes.c_size_t(-1).value
     assert lib.fa_paged_workspace_size(4, 1, 8, 0, 128) == ctypes.c_size_t(-1).value
 
