@@ -379,7 +379,12 @@ int fa_paged_attention(const fa_paged_attention_args* args, void* stream) {
       !steps(c.v_head, c.heads) || !steps(c.v_page, c.num_pages))
     return FA_ERR_UNSUPPORTED;
   const int max_q = r.max_q < c.tokens ? r.max_q : c.tokens;
+  // the split counts key tiles of items in 32 bits
   const Workspace ws = workspace_for(max_q, group, c.d);
+  const int tpi = ws.rows == fa::kChunkRows ? 2 * (fa::kKeyTile / group) : max_q;
+  const long long items = c.tokens / tpi + c.batch;
+  const long long tiles = static_cast<long long>(c.table_width) * c.page_size / fa::kKeyTile + 2;
+  if (items * c.heads > fa::kMaxCost / (tiles + fa::kItemCost)) return FA_ERR_UNSUPPORTED;
   if (!ok_ptr(r.workspace, 256) || r.workspace_bytes < ws.bytes) return FA_ERR_INVALID;
   const AttentionArgs a{&c,
                         r.q,

@@ -16,13 +16,20 @@
 // hands registers to warpgroups 0 and 1):
 //   warps 0-3, 4-7  softmax of query tile 0 and 1: thread r owns row r (TMEM lane r) and
 //                   the tile's 128 scores of it, so its maximum needs no exchange.
-//   warp 8          K producer: the item's two Q tiles, then K tiles into 3 stages.
+//   warp 8          K producer: the item's two Q tiles, then K tiles into 2 stages.
 //   warp 10         V producer, 2 stages. Both walk the page table by themselves, a window
 //                   of pages ahead, one box per page and 64 columns.
+//   warp 11         scheduler: the CTA's items.
 //   warp 9          MMA issuer, in the order S0_j S1_j | PV0_j S0_j+1 PV1_j S1_j+1 | ...,
 //                   so that one warpgroup exponentiates while the tensor core multiplies
 //                   for the other. The order runs on across items: the next item's first
 //                   scores are computed while this one's outputs are stored.
+//
+// An item with one query tile (a single token among chunks, a short draft, a chunk's last
+// tokens) would leave one warpgroup idle and the tensor core waiting for the other. There
+// the two take the key tiles in turn, both with query tile 0 (order S0_j S1_j+1 PV0_j
+// S0_j+2 PV1_j+1 ...), and warpgroup 0 joins the two partial outputs out of tensor memory
+// by their log-sum-exps. Warps none of whose rows is a real query skip the softmax.
 //
 // TMEM (512 columns at d = 128): S and P of warpgroup g at 128 g, O of g at 256 + d g. MMAs
 // of one thread run in order, so S_g,j+1 complete implies P_g,j V_j complete and O_g may be
@@ -33,14 +40,12 @@
 // item sees are zeroed in shared memory before they are multiplied by weights of 0.
 #pragma once
 
-#include <type_traits>
-
 #include "fa_paged_step.cuh"
 
 namespace fa {
 
 constexpr int kChunkThreads = 384;
-constexpr int kChunkKWarp = 8, kChunkMmaWarp = 9, kChunkVWarp = 10;
+constexpr int kChunkKWarp = 8, kChunkMmaWarp = 9, kChunkVWarp = 10, kChunkScheduler = 11;
 // 168 registers per thread at launch (the most 384 threads can have), then per
 // sub-partition 2 x 216 (softmax) + 72 (producers, MMA) = 3 x 168.
 constexpr int kChunkLaunchRegs = 168;
@@ -49,7 +54,7 @@ constexpr int kChunkSmallRegs = 72;
 static_assert(2 * kChunkSoftmaxRegs + kChunkSmallRegs == 3 * kChunkLaunchRegs, "register split");
 constexpr float kChunkRescaleSlack = 8.0f;
 constexpr int kChunkRows = 256;  // rows of an item
-constexpr int kChunkKStages = 3;
+constexpr int kChunkKStages = 2;
 constexpr int kChunkVStages = 2;
 
 template <int D>
@@ -59,45 +64,52 @@ struct ChunkLayout {
   static constexpr uint32_t kQ = 0;                        // 2 tiles
   static constexpr uint32_t kK = kQ + 2 * kTileBytes;
   static constexpr uint32_t kV = kK + kChunkKStages * kTileBytes;
-  static constexpr uint32_t kBounds = kV + kChunkVStages * kTileBytes;
-  static constexpr uint32_t kBar = kBounds + sizeof(Stretch);
+  static constexpr uint32_t kOut = kV + kChunkVStages * kTileBytes;  // 4 KB per softmax warp
+  static constexpr uint32_t kItems = kOut + 8 * 4096;
+  static constexpr uint32_t kJoin = kItems + kItemSlots * sizeof(Item);  // [row] of group 1
+  static constexpr uint32_t kBar = kJoin + 128 * 8;
   static constexpr int bQFull = 0, bQEmpty = 1, bKFull = 2, bKEmpty = bKFull + kChunkKStages,
                        bVFull = bKEmpty + kChunkKStages, bVEmpty = bVFull + kChunkVStages,
                        bSFull = bVEmpty + kChunkVStages, bPFull = bSFull + 2,
-                       bPHalf = bPFull + 2, bODone = bPHalf + 2, kNumBars = bODone + 2;
+                       bPHalf = bPFull + 2, bODone = bPHalf + 2, bJoin = bODone + 2,
+                       bJoined = bJoin + 1, bItems = bJoined + 1,
+                       kNumBars = bItems + 2 * kItemSlots;
   static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
   static constexpr uint32_t kAbort = kTmemSlot + 8;
   static constexpr uint32_t kBytes = kAbort + 8 + 1024;
-  // at least 120 KB, so that one CTA and its 512 TMEM columns sit on each SM; and the
-  // split's scratch (8 bytes per sequence) fits before the bounds
-  static constexpr uint32_t kSmem = kBytes > 136 * 1024 ? kBytes : 136 * 1024;
+  // at least 120 KB, so that one CTA and its 512 TMEM columns sit on each SM
+  static constexpr uint32_t kSmem = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
   static constexpr uint32_t tS = 0;    // + 128 * warpgroup
   static constexpr uint32_t tO = 256;  // + D * warpgroup
 };
 
-// The key tiles that each query tile of an item takes part in, within the CTA's part.
+// The key tiles that each warpgroup of an item takes part in, within the CTA's part.
 struct ChunkTiles {
-  int lo[2], hi[2];  // [lo, hi); lo >= hi: none
+  bool one;          // one query tile: group g takes tiles first + g, first + g + 2, ...
+  int lo[2], hi[2];  // otherwise query tile g takes [lo, hi); lo >= hi: none
   int first, last;   // the union, [first, last)
 
-  __device__ __forceinline__ ChunkTiles(const Walk& w, int tpt, int wl, int wr) {
+  __device__ __forceinline__ ChunkTiles(const Item& w, int tpt, int wl, int wr) {
     first = w.keys.first + w.j0;
     last = w.keys.first + w.j1;
+    one = (2 * w.p + 1) * tpt >= w.n;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const int p = 2 * w.at.p + g;
-      const KeyRange r = p * tpt < w.seq.n ? item_keys(p, tpt, w.seq.n, w.seq.nk, wl, wr)
-                                           : KeyRange{0, -1, 0, 0};
+      const KeyRange r = one ? KeyRange{0, 0, first + g, last - first - g}
+                             : item_keys(2 * w.p + g, tpt, w.n, w.nk, wl, wr);
       lo[g] = max(first, r.first);
       hi[g] = min(last, r.first + r.count);
     }
   }
+  __device__ __forceinline__ int step() const { return one ? 2 : 1; }
   __device__ __forceinline__ bool in(int g, int tile) const {
-    return g ? tile >= lo[1] && tile < hi[1] : tile >= lo[0] && tile < hi[0];
+    const int l = g ? lo[1] : lo[0], h = g ? hi[1] : hi[0];
+    return tile >= l && tile < h && (!one || ((tile - l) & 1) == 0);
   }
-  __device__ __forceinline__ int count(int g) const {
-    return max(0, g ? hi[1] - lo[1] : hi[0] - lo[0]);
+  __device__ __forceinline__ bool last_of(int g, int tile) const {
+    return tile + step() >= (g ? hi[1] : hi[0]);
   }
+  __device__ __forceinline__ bool any(int g) const { return g ? lo[1] < hi[1] : lo[0] < hi[0]; }
 };
 
 template <int D, bool BF16>
@@ -113,7 +125,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   using Lay = ChunkLayout<D>;
   // Of every 16 exponential pairs, two go to the FMA pipe at d = 128, none at d = 64, and
   // at d = 64 P V is issued in two halves: measured on the contiguous forward, whose inner
-  // loop this is.
+  // loop this is. (Masked scores may take the polynomial: its 2^-125 for them vanishes next
+  // to the row's own weights, and in a row without any nothing is read.)
   constexpr int kPolyPairs = D == 64 ? 0 : 2;
   constexpr int kPolyStride = kPolyPairs > 0 ? 16 / kPolyPairs : 16;
   constexpr bool kSplitPV = D == 64;
@@ -125,10 +138,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int tpt = kKeyTile / group;  // tokens of a query tile
+  // x / group for x < 128: ceil(2^16 / group) errs by less than 128 / 2^16 of a unit
+  const int by_group = (65535 + group) / group;
   const int tpi = 2 * tpt;           // tokens of an item
   auto bar = [&](int i) -> uint32_t { return sbase + Lay::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbort);
-  Stretch* bounds = reinterpret_cast<Stretch*>(smem + Lay::kBounds);
 
   dependents_may_launch();
   if (threadIdx.x == 0) {
@@ -148,6 +162,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(bar(Lay::bPHalf + g), 128);
       mbar_init(bar(Lay::bODone + g), 1);
     }
+    mbar_init(bar(Lay::bJoin), 128);
+    mbar_init(bar(Lay::bJoined), 128);
+    item_ring_init(bar(Lay::bItems), 11);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -155,23 +172,31 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     tmem_alloc(sbase + Lay::kTmemSlot, 512);
     tmem_relinquish();
   }
-  // scratch of the split lies behind the Q tiles, whose rows no box fills stay zero
-  for (uint32_t i = threadIdx.x; i < 2 * Lay::kTileBytes / 16; i += kChunkThreads)
-    *reinterpret_cast<uint4*>(smem + Lay::kQ + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-  tc_fence_before();
+  // rows of the Q tiles that no box fills stay zero
+  if (tpt * group < kKeyTile)
+    for (uint32_t i = threadIdx.x; i < 2 * Lay::kTileBytes / 16; i += kChunkThreads)
+      *reinterpret_cast<uint4*>(smem + Lay::kQ + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_async_smem();
   dependency_wait();
-  split_bounds<false>(c, tpi, max_q, wl, wr, least,
-                      reinterpret_cast<long long*>(smem + Lay::kK), bounds);
+  Scheduler<false> schedule(c, tpi, max_q, wl, wr);
+  if (warp == kChunkScheduler) schedule.locate(least);
+  tc_fence_before();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Lay::kTmemSlot);
+  ItemRing ring(sbase + Lay::kItems, bar(Lay::bItems));
+  Item w;
+  bool ok = true;
 
   if (warp >= 8) setmaxnreg_dec<kChunkSmallRegs>();  // every warp of warpgroup 2
-  if (warp == kChunkKWarp || warp == kChunkVWarp) {
+  if (warp == kChunkScheduler) {
+    schedule.run(ring, abort_flag, parts);
+  } else if (warp == kChunkKWarp || warp == kChunkVWarp) {
     // ---------------------------------------------------------------- producers
     const bool is_k = warp == kChunkKWarp;
     const CUtensorMap* map = is_k ? &tmK : &tmV;
     const int stages = is_k ? kChunkKStages : kChunkVStages;
-    const uint32_t ring = sbase + (is_k ? Lay::kK : Lay::kV);
+    const uint32_t tiles = sbase + (is_k ? Lay::kK : Lay::kV);
     const int full = is_k ? Lay::bKFull : Lay::bVFull, empty = is_k ? Lay::bKEmpty : Lay::bVEmpty;
     if (lane == 0) {
       tma_prefetch(map);
@@ -180,14 +205,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncwarp();
     int st = 0, item = 0;
     uint32_t phase = 1;  // of the stage's empty barrier: the first pass finds it free
-    bool ok = true;
     PageWindow win;
     win.bad = false;
-    for (Walk w(c, tpi, max_q, wl, wr, *bounds); w.more && ok;
-         w.next(c, tpi, max_q, wl, wr)) {
+    while (ok && __all_sync(0xffffffffu, ring.get(&w, &ok, abort_flag))) {
+      ring.read(lane == 0);
       if (w.j0 >= w.j1) continue;
       const int first = w.keys.first + w.j0;
-      win.start(c, w.at.b, first * kKeyTile >> c.page_shift, lane);
+      win.start(c, w.b, first * kKeyTile >> c.page_shift, lane);
       if (is_k) {
         ok = item == 0 ||
              mbar_wait(bar(Lay::bQEmpty), static_cast<uint32_t>(item - 1) & 1, abort_flag);
@@ -196,15 +220,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           break;
         }
         if (lane == 0) {
-          const ChunkTiles t(w, tpt, wl, wr);
-          const uint32_t bytes = static_cast<uint32_t>(tpt) * group * D * 2;
-          mbar_expect_tx(bar(Lay::bQFull), ((t.count(0) > 0) + (t.count(1) > 0)) * bytes);
-          for (int g = 0; g < 2; ++g)
-            if (t.count(g) > 0)
-              for (int i = 0; i < D / 64; ++i)
-                tma_load_4d(sbase + Lay::kQ + g * Lay::kTileBytes + i * Lay::kChunkBytes, &tmQ,
-                            i * 64, 0, w.seq.begin + (2 * w.at.p + g) * tpt, w.at.h,
-                            bar(Lay::bQFull));
+          // both tiles, or the only one
+          const int q_tiles = (2 * w.p + 1) * tpt >= w.n ? 1 : 2;
+          mbar_expect_tx(bar(Lay::bQFull), static_cast<uint32_t>(q_tiles * tpt * group) * D * 2);
+          for (int g = 0; g < q_tiles; ++g)
+            for (int i = 0; i < D / 64; ++i)
+              tma_load_4d(sbase + Lay::kQ + g * Lay::kTileBytes + i * Lay::kChunkBytes, &tmQ,
+                          i * 64, 0, w.begin + (2 * w.p + g) * tpt, w.h, bar(Lay::bQFull));
         }
         __syncwarp();
         ++item;
@@ -220,8 +242,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           mbar_expect_tx(bar(full + st),
                          static_cast<uint32_t>(pages.count * pages.rows) * D * 2);
         __syncwarp();
-        load_tile_pages<D>(pages, tile, c.page_shift, win, map, ring + st * Lay::kTileBytes,
-                           bar(full + st), nullptr, 0, 0, w.at.h, lane);
+        load_tile_pages<D>(pages, tile, c.page_shift, win, map, tiles + st * Lay::kTileBytes,
+                           bar(full + st), nullptr, 0, 0, w.h, lane);
         if (++st == stages) {
           st = 0;
           phase ^= 1;
@@ -229,13 +251,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
     if (win.bad) atomicExch(&g_fa_status, kStatusInvalid);
-    if (is_k && lane == 0) write_part_info(c, tpi, max_q, *bounds, parts);
   } else if (warp == kChunkMmaWarp) {
     // -------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_f16_f32(kKeyTile, kKeyTile, BF16, false, false);
       constexpr uint32_t idesc_o = idesc_f16_f32(kKeyTile, D, BF16, false, true);
-      bool ok = true;
       int ks = 0, vs = 0, item = 0;
       uint32_t kphase = 0, vphase = 0;
       uint32_t pphase[2] = {0, 0};
@@ -269,43 +289,57 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         return true;
       };
       bool v_owed = false;  // the previous tile's V stage is to be released
-      for (Walk w(c, tpi, max_q, wl, wr, *bounds); w.more && ok;
-           w.next(c, tpi, max_q, wl, wr)) {
+      while (ok && ring.get(&w, &ok, abort_flag)) {
+        ring.read(true);
         if (w.j0 >= w.j1) continue;
         const ChunkTiles t(w, tpt, wl, wr);
         bool q_waited = false;
         for (int tile = t.first; ok && tile < t.last; ++tile) {
           bool v_waited = false, k_waited = false;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
+          auto owing = [&](int g) {
             if (ok && owed[g]) {
               ok = product(g, !v_waited);
               v_waited = true;
             }
-            if (ok && t.in(g, tile)) {
-              if (!q_waited) {
-                ok = mbar_wait(bar(Lay::bQFull), static_cast<uint32_t>(item) & 1, abort_flag);
-                q_waited = true;
-              }
-              if (ok && !k_waited) {
-                ok = mbar_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
-                k_waited = true;
-              }
-              if (ok) {
-                tc_fence_after();
-                const uint64_t dq = sdesc_sw128(sbase + Lay::kQ + g * Lay::kTileBytes, 16, 1024);
-                const uint64_t dk = sdesc_sw128(sbase + Lay::kK + ks * Lay::kTileBytes, 16, 1024);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                  const uint32_t koff = (k >> 2) * Lay::kChunkBytes + (k & 3) * 32;
-                  mma_ss(tmem + Lay::tS + g * 128, sdesc_step(dq, koff), sdesc_step(dk, koff),
-                         idesc_s, k > 0 ? 1u : 0u);
-                }
-                mma_commit(bar(Lay::bSFull + g));
-                const int lo = g ? t.lo[1] : t.lo[0], hi = g ? t.hi[1] : t.hi[0];
-                owed[g] = (tile == lo ? 1 : 2) + (tile == hi - 1 ? 4 : 0);
-              }
+          };
+          auto scores = [&](int g) {
+            if (!ok || !t.in(g, tile)) return;
+            if (!q_waited) {
+              ok = mbar_wait(bar(Lay::bQFull), static_cast<uint32_t>(item) & 1, abort_flag);
+              q_waited = true;
             }
+            if (ok && !k_waited) {
+              ok = mbar_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
+              k_waited = true;
+            }
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t dq =
+                sdesc_sw128(sbase + Lay::kQ + (t.one ? 0 : g) * Lay::kTileBytes, 16, 1024);
+            const uint64_t dk = sdesc_sw128(sbase + Lay::kK + ks * Lay::kTileBytes, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t koff = (k >> 2) * Lay::kChunkBytes + (k & 3) * 32;
+              mma_ss(tmem + Lay::tS + g * 128, sdesc_step(dq, koff), sdesc_step(dk, koff), idesc_s,
+                     k > 0 ? 1u : 0u);
+            }
+            mma_commit(bar(Lay::bSFull + g));
+            owed[g] = (tile == (g ? t.lo[1] : t.lo[0]) ? 1 : 2) + (t.last_of(g, tile) ? 4 : 0);
+          };
+          // the previous tile's products and this one's scores; with one query tile the
+          // scores (of the other group than the product) go first
+          const int turns = t.one && tile > t.first;
+          if (turns && ((tile - t.first) & 1)) {
+            scores(1);
+            owing(0);
+          } else if (turns) {
+            scores(0);
+            owing(1);
+          } else {
+            owing(0);
+            scores(0);
+            owing(1);
+            scores(1);
           }
           if (!ok) break;
           mma_commit(bar(Lay::bKEmpty + ks));
@@ -339,39 +373,92 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int g = warp >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row of the query tile = TMEM lane
-    const int tr = r / group;           // its token in the tile (tpt or more: a row of zeros)
+    const int tr = r * by_group >> 16;  // its token in the tile (tpt or more: a row of zeros)
     const int head_in = r - tr * group;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t s_cols = Lay::tS + g * 128;
     const uint32_t o_cols = Lay::tO + g * D;
     const uint64_t c2 = f2_pack(scale_log2, scale_log2);
-    bool ok = true;
-    uint32_t sphase = 0, ophase = 0;
+    uint32_t sphase = 0, ophase = 0, jphase = 0;
     int vi = 0;  // V tiles of the CTA before this item
-    for (Walk w(c, tpi, max_q, wl, wr, *bounds); w.more && ok;
-         w.next(c, tpi, max_q, wl, wr)) {
-      const int tok0 = (2 * w.at.p + g) * tpt;  // first token of the query tile
-      const int off = w.seq.nk - w.seq.n;
-      int lo = 0, hi = 0, first = 0;
-      if (w.j1 > w.j0) {
+    while (ok) {
+      if (!__all_sync(0xffffffffu, ring.get(&w, &ok, abort_flag))) break;
+      ring.read(lane == 0);
+      const int off = w.nk - w.n;
+      bool one;
+      int lo, hi, first;
+      {
         const ChunkTiles t(w, tpt, wl, wr);
+        one = t.one;
         lo = g ? t.lo[1] : t.lo[0];
         hi = g ? t.hi[1] : t.hi[0];
         first = t.first;
       }
+      const int step = one ? 2 : 1;
+      const int tok0 = (2 * w.p + (one ? 0 : g)) * tpt;  // first token of the query tile
+      // whether any row of this warp is a query
+      const bool busy = quarter * 32 < min(tpt, w.n - tok0) * group;
       // keys that every row of the query tile sees, and this thread's row
-      const int all_lo = min(tok0 + tpt, w.seq.n) - 1 + off - wl;
-      const int all_hi = min(w.seq.nk - 1, tok0 + off + wr);
+      const int all_lo = min(tok0 + tpt, w.n) - 1 + off - wl;
+      const int all_hi = min(w.nk - 1, tok0 + off + wr);
       const int mid = tok0 + tr + off;
-      const int row_lo = mid - wl, row_hi = min(w.seq.nk - 1, mid + wr);
+      const int row_lo = mid - wl, row_hi = min(w.nk - 1, mid + wr);
       float m = -INFINITY;  // running reference, base-2 scaled units
       float l = 0.f;        // row sum of p
       float l_o = 0.f;      // row sum of the 16-bit-rounded p
-      for (int tile = lo; tile < hi; ++tile) {
+      for (int tile = lo; ok && tile < hi; tile += step) {
         ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bSFull + g), sphase, abort_flag));
         if (!ok) break;
         sphase ^= 1;
         tc_fence_after();
+        const int key0 = tile * kKeyTile;
+        const bool edge = key0 < all_lo || key0 + kKeyTile - 1 > all_hi;
+        if (edge && (key0 < w.keys.lo || key0 + kKeyTile - 1 > w.keys.hi)) {
+          // keys that no row of the item sees: their V rows become zeros (by all warps)
+          const int v = vi + tile - first;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(bar(Lay::bVFull + v % kChunkVStages),
+                                    static_cast<uint32_t>(v / kChunkVStages) & 1, abort_flag));
+          if (!ok) break;
+          if (key0 + r < w.keys.lo || key0 + r > w.keys.hi) {
+            const uint32_t row = sbase + Lay::kV + (v % kChunkVStages) * Lay::kTileBytes + r * 128;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                               row + (i >> 3) * Lay::kChunkBytes + (i & 7) * 16),
+                           "r"(0)
+                           : "memory");
+          }
+          fence_async_smem();
+        }
+        if (!busy) {
+          tc_fence_before();
+          if (kSplitPV) mbar_arrive(bar(Lay::bPHalf + g));
+          mbar_arrive(bar(Lay::bPFull + g));
+          continue;
+        }
+        // An edge of the mask: columns [first_col, last_col] of the row are visible, the
+        // others become -inf in tensor memory. 32 columns at a time in a loop, off the main
+        // path: unrolled on the registers below it tripled an edge tile's time, most of it
+        // spent fetching instructions that few tiles run.
+        if (edge) {
+          const int first_col = row_lo - key0, last_col = row_hi - key0;
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            const int lo_bit = first_col - 32 * h, hi_bit = last_col - 32 * h;
+            uint32_t seen = hi_bit < 0 ? 0u : 0xffffffffu >> (31 - min(hi_bit, 31));
+            seen &= lo_bit > 31 ? 0u : 0xffffffffu << max(lo_bit, 0);
+            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+            uint32_t x[32];
+            tmem_ld32(lane_base + s_cols + h * 32, x);
+            tmem_wait_ld();
+            reg_fence32(x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1 ? x[i] : 0xff800000u;
+            tmem_st32(lane_base + s_cols + h * 32, x);
+          }
+          tmem_wait_st();
+        }
         float s[128];
         {
           uint32_t sr[128];
@@ -382,33 +469,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int i = 0; i < 4; ++i) reg_fence32(sr + i * 32);
 #pragma unroll
           for (int e = 0; e < 128; ++e) s[e] = __uint_as_float(sr[e]);
-        }
-        const int key0 = tile * kKeyTile;
-        const bool edge = key0 < all_lo || key0 + kKeyTile - 1 > all_hi;
-        if (edge) {
-          const int first_col = row_lo - key0, last_col = row_hi - key0;
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            s[i] = (i > last_col || i < first_col) ? -INFINITY : s[i];
-          const int key = key0 + r;
-          if (key0 < w.keys.lo || key0 + kKeyTile - 1 > w.keys.hi) {  // the same for all threads
-            const int v = vi + tile - first;
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait(bar(Lay::bVFull + v % kChunkVStages),
-                                      static_cast<uint32_t>(v / kChunkVStages) & 1, abort_flag));
-            if (!ok) break;
-            if (key < w.keys.lo || key > w.keys.hi) {
-              const uint32_t row =
-                  sbase + Lay::kV + (v % kChunkVStages) * Lay::kTileBytes + r * 128;
-#pragma unroll
-              for (int i = 0; i < D / 8; ++i)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 row + (i >> 3) * Lay::kChunkBytes + (i & 7) * 16),
-                             "r"(0)
-                             : "memory");
-            }
-            fence_async_smem();
-          }
         }
         // row maximum over four independent chains
         float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -441,42 +501,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         };
         if (kSplitPV) rescale_o();
         uint64_t sum2[2] = {0, 0}, sum2_o[2] = {0, 0};  // packed +0.0f
-        auto exps = [&](auto poly_tag) {
-          constexpr bool kPoly = decltype(poly_tag)::value;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t pk[16];
+        for (int h = 0; h < 4; ++h) {
+          uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int e = h * 32 + 2 * i;
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, nm2), x0, x1);
-              float p0, p1;
-              if (kPoly && i % kPolyStride == kPolyStride - 1) {
-                ex2_poly_pair(x0, x1, p0, p1);
-              } else {
-                p0 = ex2_approx(x0);
-                p1 = ex2_approx(x1);
-              }
-              pk[i] = pack2<BF16>(p0, p1);
-              float r0, r1;
-              unpack2<BF16>(pk[i], r0, r1);
-              sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
-              sum2_o[i & 1] = f2_add(sum2_o[i & 1], f2_pack(r0, r1));
+          for (int i = 0; i < 16; ++i) {
+            const int e = h * 32 + 2 * i;
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, nm2), x0, x1);
+            float p0, p1;
+            if (kPolyPairs > 0 && i % kPolyStride == kPolyStride - 1) {
+              ex2_poly_pair(x0, x1, p0, p1);
+            } else {
+              p0 = ex2_approx(x0);
+              p1 = ex2_approx(x1);
             }
-            tmem_st16(lane_base + s_cols + h * 16, pk);
-            if (kSplitPV && h == 1) {  // keys 0-63 (and a rescaled O) are in TMEM
-              tmem_wait_st();
-              tc_fence_before();
-              mbar_arrive(bar(Lay::bPHalf + g));
-            }
+            pk[i] = pack2<BF16>(p0, p1);
+            float r0, r1;
+            unpack2<BF16>(pk[i], r0, r1);
+            sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
+            sum2_o[i & 1] = f2_add(sum2_o[i & 1], f2_pack(r0, r1));
           }
-        };
-        // masked tiles stay on the MUFU, which returns exact zeros for them
-        if (kPolyPairs > 0 && !edge)
-          exps(std::integral_constant<bool, true>{});
-        else
-          exps(std::integral_constant<bool, false>{});
+          tmem_st16(lane_base + s_cols + h * 16, pk);
+          if (kSplitPV && h == 1) {  // keys 0-63 (and a rescaled O) are in TMEM
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(Lay::bPHalf + g));
+          }
+        }
         float a0, a1, b0, b1;
         f2_unpack(f2_add(sum2[0], sum2[1]), a0, a1);
         f2_unpack(f2_add(sum2_o[0], sum2_o[1]), b0, b1);
@@ -489,60 +541,134 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         m = m_new;
       }
       vi += w.j1 - w.j0;
-      // O / l_o straight from the row's thread to its place
-      if (hi > lo) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(Lay::bODone + g), ophase, abort_flag));
-        if (!ok) break;
-        ophase ^= 1;
-        tc_fence_after();
-      }
-      const int ti = tok0 + tr;
-      const bool live = tr < tpt && ti < w.seq.n;
-      const bool whole = w.j0 == 0 && w.j1 == w.keys.count;
-      const long prow = (w.j0 > 0 ? 2L * blockIdx.x : 2L * blockIdx.x + 1) * kChunkRows +
-                        (g * tpt + tr) * group + head_in;
-      const int head = w.at.h * group + head_in;
-      const long orow = w.seq.begin + ti;
-      uint16_t* dst = O + orow * so.sn + head * so.sh;
-      float* part = Opart + prow * D;
-      const float inv_l = l_o > 0.f ? 1.f / l_o : 0.f;  // rows that see no key: O = 0
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t o[32];
-        if (hi > lo) {  // without a key tile O was never written
-          tmem_ld32(lane_base + o_cols + i * 32, o);
-          tmem_wait_ld();
-          reg_fence32(o);
+      const bool some = lo < hi;
+      ok = __all_sync(0xffffffffu, ok && (!some || mbar_wait(bar(Lay::bODone + g), ophase,
+                                                            abort_flag)));
+      ophase ^= some;
+      tc_fence_after();
+      // rows that see no key: O = 0, L = -inf (their sums need not be 0: the polynomial's
+      // least value is 2^-125)
+      const bool none = m == -INFINITY;
+      float L2 = none ? -INFINITY : m + log2f(l);
+      float inv_l = none || l_o == 0.f ? 0.f : 1.f / l_o;
+      float inv_other = 0.f;
+      float2* join = reinterpret_cast<float2*>(smem + Lay::kJoin);
+      if (one && ok) {  // group 1 hands over
+        if (g == 1) {
+          join[r] = make_float2(L2, inv_l);
+          mbar_arrive(bar(Lay::bJoin));
         } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        if (live && whole) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t hw[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              hw[k] = pack2<BF16>(__uint_as_float(o[8 * e + 2 * k]) * inv_l,
-                                  __uint_as_float(o[8 * e + 2 * k + 1]) * inv_l);
-            *reinterpret_cast<uint4*>(dst + i * 32 + e * 8) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bJoin), jphase, abort_flag));
+          tc_fence_after();
+          const float2 other = join[r];
+          const float top = fmaxf(L2, other.x);
+          if (top != -INFINITY) {
+            const float f = ex2_approx(L2 - top), fo = ex2_approx(other.x - top);
+            const float inv = 1.f / (f + fo);
+            inv_l *= f * inv;
+            inv_other = other.y * fo * inv;
+            L2 = top + log2f(f + fo);
           }
-        } else if (live) {
+        }
+      }
+      // O / l_o: a thread holds a row, a store wants rows' neighbours side by side, so 128
+      // bytes of each row (64 columns, or 32 of a part in fp32) at a time go through the
+      // warp's 4 KB of shared memory, 16-byte pieces swizzled by row, and leave as four
+      // rows of 128 bytes an instruction. (Straight from the rows' threads an item's store
+      // took 3000 to 8000 cycles, this one about 900.)
+      if (ok && busy && !(one && g == 1)) {
+        const bool whole = w.j0 == 0 && w.j1 == w.keys.count;
+        const bool other_some = one && first + 1 < w.keys.first + w.j1;
+        const int rows = min(tpt, w.n - tok0) * group;  // of the query tile
+        const int row0 = quarter * 32;
+        const long slot_row = (w.j0 > 0 ? 2L * blockIdx.x : 2L * blockIdx.x + 1) * kChunkRows +
+                              (one ? 0 : g) * tpt * group;
+        const uint32_t stage = sbase + Lay::kOut + warp * 4096;
+        const int piece = lane & 7;
+                uint16_t* out = O + static_cast<long>(w.begin + tok0) * so.sn +
+                        static_cast<long>(w.h) * group * so.sh + piece * 8;
+        float* part = Opart + (slot_row + row0 + (lane >> 3)) * D + piece * 4;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          float x[32];
+          uint32_t o[32];
+          if (some) {  // without a key tile O was never written
+            tmem_ld32(lane_base + o_cols + i, o);
+            tmem_wait_ld();
+            reg_fence32(o);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<float4*>(part + i * 32 + e * 4) =
-                make_float4(__uint_as_float(o[4 * e]) * inv_l, __uint_as_float(o[4 * e + 1]) * inv_l,
-                            __uint_as_float(o[4 * e + 2]) * inv_l,
-                            __uint_as_float(o[4 * e + 3]) * inv_l);
+            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(o[e]) * inv_l;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = 0.f;
+          }
+          if (other_some) {
+            tmem_ld32(lane_base + Lay::tO + D + i, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o[e]), inv_other, x[e]);
+          }
+          if (whole) {  // half of the row's 128 bytes; they leave after the second half
+            const int half = (i >> 5) & 1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               stage + lane * 128 + (((half * 4 + e) ^ (lane & 7)) << 4)),
+                           "r"(pack2<BF16>(x[8 * e], x[8 * e + 1])),
+                           "r"(pack2<BF16>(x[8 * e + 2], x[8 * e + 3])),
+                           "r"(pack2<BF16>(x[8 * e + 4], x[8 * e + 5])),
+                           "r"(pack2<BF16>(x[8 * e + 6], x[8 * e + 7]))
+                           : "memory");
+            if (!half) continue;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               stage + lane * 128 + ((e ^ (lane & 7)) << 4)),
+                           "f"(x[4 * e]), "f"(x[4 * e + 1]), "f"(x[4 * e + 2]), "f"(x[4 * e + 3])
+                           : "memory");
+          }
+          __syncwarp();
+          uint4 y[8];  // row 4 e + lane / 8 of the warp, all loaded before the first leaves
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int sr = 4 * e + (lane >> 3);
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(y[e].x), "=r"(y[e].y), "=r"(y[e].z), "=r"(y[e].w)
+                         : "r"(stage + sr * 128 + ((piece ^ (sr & 7)) << 4))
+                         : "memory");
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int row = row0 + 4 * e + (lane >> 3);  // of the query tile
+            if (row < rows) {
+              if (whole) {
+                const int t = row * by_group >> 16;
+                *reinterpret_cast<uint4*>(out + t * so.sn + (row - t * group) * so.sh + (i - 32)) =
+                    y[e];
+              } else {
+                *reinterpret_cast<uint4*>(part + 4 * e * D + i) = y[e];
+              }
+            }
+          }
+          __syncwarp();
+        }
+        if (r < rows) {
+          if (whole)
+            L[static_cast<long>(w.h * group + head_in) * c.tokens + w.begin + tok0 + tr] =
+                L2 * 0.69314718055994530942f;
+          else
+            Lpart[slot_row + r] = L2;
         }
       }
       tc_fence_before();
-      if (live) {
-        const float L2 = l > 0.f ? m + log2f(l) : -INFINITY;
-        if (whole)
-          L[static_cast<long>(head) * c.tokens + orow] = L2 * 0.69314718055994530942f;
+      if (one && ok) {  // O of group 1 has been read
+        if (g == 0)
+          mbar_arrive(bar(Lay::bJoined));
         else
-          Lpart[prow] = L2;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bJoined), jphase, abort_flag));
+        jphase ^= 1;
       }
     }
   }

@@ -11,8 +11,9 @@
 //
 // The split depends only on the lengths, the mask and the grid, so the parts and the order
 // in which they are joined -- and with them every rounding -- are the same on every call.
-// Every CTA finds its two boundaries itself (a pass over the batch's lengths, no launch of
-// its own, nothing to keep in step with the lengths): split_bounds below.
+// One warp of every CTA, the scheduler, finds the CTA's stretch from the batch's lengths (no
+// launch of its own, nothing to keep in step with the lengths) and hands the items to the
+// other warps through a ring in shared memory.
 #pragma once
 
 #ifdef __CUDACC__
@@ -49,181 +50,31 @@ __host__ __device__ inline int item_cost(const KeyRange& r) { return r.count + k
 // CTAs of an attention launch: one per SM of a B200. A fixed count keeps the split the
 // same everywhere, and divisions by it are multiplications.
 constexpr int kSplitGrid = 148;
-// A CTA's share of cost W: an even part of it, at least `least`. (Every CTA computes it in
-// its prologue, where a 64-bit division by a variable is 400 cycles of latency.)
-__host__ __device__ inline long long split_share(long long W, int least) {
-  const long long even = (W + kSplitGrid - 1) / kSplitGrid;
+// A CTA's share of cost W (which the host keeps below kMaxCost, so that 32 bits hold every
+// sum here): an even part of it, at least `least`.
+constexpr long long kMaxCost = 1LL << 31;
+__host__ __device__ inline unsigned split_share(unsigned W, unsigned least) {
+  const unsigned even = (W + kSplitGrid - 1) / kSplitGrid;
   return even > least ? even : least;
 }
 // Start of CTA c's stretch.
-__host__ __device__ inline long long split_start(long long W, int c, long long share) {
+__host__ __device__ inline unsigned split_start(unsigned W, unsigned c, unsigned share) {
   return c * share < W ? c * share : W;
 }
-// a / b of non-negative numbers, 32 bits wide where they fit.
-__host__ __device__ inline long long quotient(long long a, long long b) {
-  return (a | b) >> 32 ? a / b : static_cast<unsigned>(a) / static_cast<unsigned>(b);
-}
 // The tile at which a boundary `r` units into an item cuts it (0: before the item).
-__host__ __device__ inline int split_tile(long long r) {
-  return r <= kItemCost ? 0 : static_cast<int>(r - kItemCost);
+__host__ __device__ inline int split_tile(unsigned r) {
+  return r <= static_cast<unsigned>(kItemCost) ? 0 : static_cast<int>(r) - kItemCost;
 }
 
-// Before tile j of the item (sequence b, key head h, place p).
-struct Bound {
-  int b, h, p, j;
+// An item, or the part of it that falls to a CTA: tiles [first + j0, first + j1).
+struct __align__(16) Item {
+  int begin, n, nk, b;  // its sequence: first packed row, new tokens, keys, index
+  int h, p;             // key head, place in the sequence
+  KeyRange keys;
+  int j0, j1;
 };
 
 #ifdef __CUDACC__
-// A CTA's stretch: from `at` to before `end`; `seq` is at's sequence.
-struct Stretch {
-  Bound at, end;
-  SeqInfo seq;
-};
-
-// Called by all threads of the block. `costs`: shared scratch of 8 bytes per sequence;
-// *out: shared. Reports sequences with inconsistent lengths. Ends with a __syncthreads.
-template <bool ONE_ITEM>
-__device__ __forceinline__ void split_bounds(const PagedView& c, int tpi, int max_q, int wl,
-                                             int wr, int least, long long* costs, Stretch* out) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int warps = blockDim.x >> 5;
-  // cost per key head of every sequence
-  if (ONE_ITEM) {
-    for (int b = threadIdx.x; b < c.batch; b += blockDim.x) {
-      const SeqInfo s = seq_info(c, b, max_q);
-      if (!s.ok && blockIdx.x == 0) atomicExch(&g_fa_status, kStatusInvalid);
-      costs[b] = s.n > 0 ? item_cost(item_keys(0, tpi, s.n, s.nk, wl, wr)) : 0;
-    }
-  } else {
-    for (int b = warp; b < c.batch; b += warps) {
-      const SeqInfo s = seq_info(c, b, max_q);
-      if (!s.ok && blockIdx.x == 0 && lane == 0) atomicExch(&g_fa_status, kStatusInvalid);
-      const int items = items_of(s.n, tpi);
-      long long sum = 0;
-      for (int p = lane; p < items; p += 32)
-        sum += item_cost(item_keys(p, tpi, s.n, s.nk, wl, wr));
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (lane == 0) costs[b] = sum;
-    }
-  }
-  __syncthreads();
-  if (warp < 2) {  // warp w finds the start of CTA blockIdx.x + w
-    const int per = (c.batch + 31) / 32;
-    const int b0 = min(c.batch, lane * per), b1 = min(c.batch, b0 + per);
-    long long own = 0;
-    for (int b = b0; b < b1; ++b) own += costs[b];
-    long long upto = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += v;
-    }
-    const long long W = __shfl_sync(0xffffffffu, upto, 31) * c.heads;
-    const long long x =
-        split_start(W, static_cast<int>(blockIdx.x) + warp, split_share(W, least));
-    Bound at{c.batch, 0, 0, 0};
-    SeqInfo s{};
-    if (x < W) {
-      // the lane whose sequences hold x, then the sequence
-      const long long before = (upto - own) * c.heads;
-      const unsigned hit = __ballot_sync(0xffffffffu, before <= x && x < upto * c.heads);
-      const int from = __ffs(hit) - 1;
-      int b = b0;
-      long long rem = x - before;
-      if (lane == from)
-        while (rem >= costs[b] * c.heads) rem -= costs[b++] * c.heads;
-      b = __shfl_sync(0xffffffffu, b, from);
-      rem = __shfl_sync(0xffffffffu, rem, from);
-      const long long w = costs[b];
-      at.b = b;
-      at.h = static_cast<int>(quotient(rem, w));
-      rem -= at.h * w;
-      s = seq_info(c, b, max_q);
-      if (!ONE_ITEM) {
-        for (int p0 = 0;; p0 += 32) {  // ends: rem < w, the sum over all items
-          const int p = p0 + lane;
-          const bool real = p < items_of(s.n, tpi);
-          const int cost = real ? item_cost(item_keys(p, tpi, s.n, s.nk, wl, wr)) : 0;
-          int sum = cost;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += v;
-          }
-          const unsigned in = __ballot_sync(0xffffffffu, real && rem < sum);
-          if (in) {
-            const int l = __ffs(in) - 1;
-            at.p = p0 + l;
-            rem -= __shfl_sync(0xffffffffu, sum - cost, l);
-            break;
-          }
-          if (!__any_sync(0xffffffffu, real)) break;
-          rem -= __shfl_sync(0xffffffffu, sum, 31);
-        }
-      }
-      at.j = split_tile(rem);
-    }
-    if (lane == 0) {
-      if (warp == 0) {
-        out->at = at;
-        out->seq = s;
-      } else {
-        out->end = at;
-      }
-    }
-  }
-  fence_async_smem();  // the scratch may be written by TMA next
-  __syncthreads();
-}
-
-// A CTA's items in order. Every role of the CTA walks them by itself.
-struct Walk {
-  Bound at, end;
-  SeqInfo seq;
-  KeyRange keys;
-  int j0, j1;  // this CTA's tiles of the item, counted from keys.first
-  bool more;
-
-  __device__ __forceinline__ Walk(const PagedView& c, int tpi, int max_q, int wl, int wr,
-                                  const Stretch& s)
-      : at(s.at), end(s.end), seq(s.seq) {
-    j0 = at.j;
-    more = at.b < c.batch;
-    settle(c, tpi, wl, wr);
-  }
-  __device__ __forceinline__ bool at_end() const {
-    return at.b == end.b && at.h == end.h && at.p == end.p;
-  }
-  __device__ __forceinline__ void settle(const PagedView& c, int tpi, int wl, int wr) {
-    if (more && at_end() && end.j <= j0) more = false;
-    if (!more) return;
-    keys = item_keys(at.p, tpi, seq.n, seq.nk, wl, wr);
-    j1 = at_end() ? end.j : keys.count;
-  }
-  __device__ __forceinline__ void next(const PagedView& c, int tpi, int max_q, int wl, int wr) {
-    if (at_end()) {
-      more = false;
-      return;
-    }
-    j0 = 0;
-    if ((++at.p) * tpi >= seq.n) {
-      at.p = 0;
-      if (++at.h == c.heads) {
-        at.h = 0;
-        do {
-          if (++at.b >= c.batch) {
-            more = false;
-            return;
-          }
-          seq = seq_info(c, at.b, max_q);
-        } while (seq.n == 0);
-      }
-    }
-    settle(c, tpi, wl, wr);
-  }
-};
-
 // What CTA c left in parts, for the kernel that joins them. Slot 2 c holds the end (or
 // the middle) of an item that an earlier CTA began, slot 2 c + 1 the beginning of one that
 // a later CTA goes on with.
@@ -236,24 +87,229 @@ struct PartInfo {
   int pad[3];
 };
 
-__device__ __forceinline__ void write_part_info(const PagedView& c, int tpi, int max_q,
-                                                const Stretch& stretch, PartInfo* parts) {
-  const Bound a = stretch.at, e = stretch.end;
-  PartInfo info{};
-  const bool same = a.b == e.b && a.h == e.h && a.p == e.p;
-  if (a.b < c.batch && e.b < c.batch && e.j > 0 && !(same && e.j <= a.j)) {
-    if (same && a.j > 0) {
-      info.goes_on = 1;
-    } else {
-      const SeqInfo s = seq_info(c, e.b, max_q);
-      info.begins = 1;
-      info.token0 = s.begin + e.p * tpi;
-      info.tokens = min(tpi, s.n - e.p * tpi);
-      info.head = e.h;
+// The ring: kItemSlots items, a barrier each for "filled" (one arrival) and "read" (one
+// arrival per reading warp).
+constexpr int kItemSlots = 3;
+struct ItemRing {
+  uint32_t items;  // shared address of Item[kItemSlots]
+  uint32_t full, empty;
+  int slot;
+  uint32_t phase;  // of the slot's pass; readers wait for `phase`, the scheduler for its flip
+
+  __device__ __forceinline__ ItemRing(uint32_t items_, uint32_t bars)
+      : items(items_), full(bars), empty(bars + 8 * kItemSlots), slot(0), phase(0) {}
+  __device__ __forceinline__ void step() {
+    if (++slot == kItemSlots) {
+      slot = 0;
+      phase ^= 1;
     }
   }
-  parts[blockIdx.x] = info;
+  // By one thread.
+  __device__ __forceinline__ bool put(const Item& it, volatile int* abort_flag) {
+    if (!mbar_wait(empty + 8 * slot, phase ^ 1, abort_flag)) return false;
+    const uint32_t at = items + slot * static_cast<uint32_t>(sizeof(Item));
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(it.begin), "r"(it.n),
+                 "r"(it.nk), "r"(it.b)
+                 : "memory");
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 16), "r"(it.h), "r"(it.p),
+                 "r"(it.keys.lo), "r"(it.keys.hi)
+                 : "memory");
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 32), "r"(it.keys.first),
+                 "r"(it.keys.count), "r"(it.j0), "r"(it.j1)
+                 : "memory");
+    mbar_arrive(full + 8 * slot);
+    step();
+    return true;
+  }
+  // By a thread, or by all lanes of a warp. False: there is none left, or the wait gave up
+  // (*ok turns false). read() tells the scheduler, once per warp.
+  __device__ __forceinline__ bool get(Item* it, bool* ok, volatile int* abort_flag) {
+    if (!mbar_wait(full + 8 * slot, phase, abort_flag)) {
+      *ok = false;
+      return false;
+    }
+    const uint32_t at = items + slot * static_cast<uint32_t>(sizeof(Item));
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(it->begin), "=r"(it->n), "=r"(it->nk), "=r"(it->b)
+                 : "r"(at)
+                 : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(it->h), "=r"(it->p), "=r"(it->keys.lo), "=r"(it->keys.hi)
+                 : "r"(at + 16)
+                 : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(it->keys.first), "=r"(it->keys.count), "=r"(it->j0), "=r"(it->j1)
+                 : "r"(at + 32)
+                 : "memory");
+    return it->begin >= 0;
+  }
+  __device__ __forceinline__ void read(bool speaker) {
+    if (speaker) mbar_arrive(empty + 8 * slot);
+    step();
+  }
+};
+__device__ __forceinline__ void item_ring_init(uint32_t bars, int readers) {
+  for (int i = 0; i < kItemSlots; ++i) {
+    mbar_init(bars + 8 * i, 1);
+    mbar_init(bars + 8 * (kItemSlots + i), static_cast<uint32_t>(readers));
+  }
 }
+
+// The scheduler: one warp. locate() reads the batch's lengths and finds the CTA's stretch;
+// run() puts its items into the ring and writes its PartInfo. ONE_ITEM: every sequence has
+// at most tpi new tokens. A CTA's first key waits for locate(), whose instructions come
+// cold from L2 at about 17 cycles each: few of them matter more than their kind.
+template <bool ONE_ITEM>
+struct Scheduler {
+  const PagedView& c;
+  const int tpi, max_q, wl, wr, lane;
+  int base;       // lane i holds sequence base + i
+  SeqInfo seq;
+  unsigned x0, x1;  // the stretch
+  int b, h, p;      // the item at x0
+  unsigned at;      // where it starts
+
+  __device__ __forceinline__ Scheduler(const PagedView& c_, int tpi_, int max_q_, int wl_, int wr_)
+      : c(c_), tpi(tpi_), max_q(max_q_), wl(wl_), wr(wr_), lane(threadIdx.x & 31) {}
+
+  __device__ __forceinline__ void load(int from) {
+    base = from;
+    const int i = from + lane;
+    seq = SeqInfo{0, 0, 0, true};
+    if (i < c.batch) seq = seq_info(c, i, max_q);
+  }
+  __device__ __forceinline__ unsigned cost_of(int place, int n, int nk) const {
+    return static_cast<unsigned>(item_cost(item_keys(place, tpi, n, nk, wl, wr)));
+  }
+  // Cost per key head of this lane's sequence.
+  __device__ __forceinline__ unsigned seq_cost() const {
+    if (ONE_ITEM) return seq.n > 0 ? cost_of(0, seq.n, seq.nk) : 0;
+    unsigned sum = 0;
+    // sequence by sequence, its items over the lanes
+    for (unsigned todo = __ballot_sync(0xffffffffu, seq.n > 0); todo; todo &= todo - 1) {
+      const int l = __ffs(todo) - 1;
+      const int n = __shfl_sync(0xffffffffu, seq.n, l), nk = __shfl_sync(0xffffffffu, seq.nk, l);
+      unsigned part = 0;
+      for (int i = lane; i * tpi < n; i += 32) part += cost_of(i, n, nk);
+      part = __reduce_add_sync(0xffffffffu, part);
+      if (lane == l) sum = part;
+    }
+    return sum;
+  }
+
+  __device__ __forceinline__ void locate(unsigned least) {
+    unsigned per_head = 0, own = 0;
+    for (int i = 0; i < c.batch; i += 32) {
+      load(i);
+      if (!seq.ok && blockIdx.x == 0) atomicExch(&g_fa_status, kStatusInvalid);
+      own = seq_cost();
+      per_head += __reduce_add_sync(0xffffffffu, own);
+    }
+    const unsigned W = per_head * c.heads;
+    const unsigned share = split_share(W, least);
+    x0 = split_start(W, blockIdx.x, share);
+    x1 = split_start(W, blockIdx.x + 1, share);
+    at = x0;
+    b = c.batch;
+    h = p = 0;
+    if (x0 >= x1) return;
+    // the sequence that holds x0
+    unsigned before = 0;
+    for (int i = 0;; i += 32) {
+      if (c.batch > 32) {
+        load(i);
+        own = seq_cost();
+      }
+      unsigned upto = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const unsigned v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, x0 < before + upto * c.heads);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        b = i + l;
+        const unsigned w = __shfl_sync(0xffffffffu, own, l);
+        unsigned r = x0 - before - (__shfl_sync(0xffffffffu, upto, l) - w) * c.heads;
+        if (r >= w) {
+          h = static_cast<int>(r / w);
+          r -= h * w;
+        }
+        if (!ONE_ITEM) r = locate_item(l, r);
+        at = x0 - r;
+        return;
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31) * c.heads;
+    }
+  }
+  // Sets p to the item of lane l's sequence that holds r; returns the rest.
+  __device__ __forceinline__ unsigned locate_item(int l, unsigned r) {
+    const int n = __shfl_sync(0xffffffffu, seq.n, l), nk = __shfl_sync(0xffffffffu, seq.nk, l);
+    for (int i = lane;; i += 32) {  // ends: r is below the sum over all items
+      unsigned sum = i * tpi < n ? cost_of(i, n, nk) : 0;
+      const unsigned cost = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const unsigned v = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += v;
+      }
+      const unsigned in = __ballot_sync(0xffffffffu, r < sum);
+      const int k = in ? __ffs(in) - 1 : 31;
+      if (in) {
+        p = i - lane + k;
+        return r - __shfl_sync(0xffffffffu, sum - cost, k);
+      }
+      r -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+
+  __device__ __forceinline__ void run(ItemRing& ring, volatile int* abort_flag, PartInfo* parts) {
+    PartInfo info{};
+    Item it;
+    bool ok = true;
+    while (ok && b < c.batch) {
+      // all lanes hold the same item
+      it.begin = __shfl_sync(0xffffffffu, seq.begin, b - base);
+      it.n = __shfl_sync(0xffffffffu, seq.n, b - base);
+      it.nk = __shfl_sync(0xffffffffu, seq.nk, b - base);
+      it.b = b;
+      bool more = it.n > 0;
+      for (; ok && more; p = 0, more = ++h < c.heads) {
+        it.h = h;
+        for (; ok && more && p * tpi < it.n; ++p) {
+          it.p = p;
+          it.keys = item_keys(p, tpi, it.n, it.nk, wl, wr);
+          const unsigned cost = item_cost(it.keys);
+          it.j0 = at < x0 ? split_tile(x0 - at) : 0;
+          it.j1 = at + cost <= x1 ? it.keys.count : split_tile(x1 - at);
+          if (it.j1 > it.j0 || (it.keys.count == 0 && at + cost <= x1)) {
+            if (it.j1 < it.keys.count) {  // a later CTA goes on with it
+              info.goes_on = it.j0 > 0;
+              info.begins = it.j0 == 0;
+              info.token0 = it.begin + p * tpi;
+              info.tokens = min(tpi, it.n - p * tpi);
+              info.head = h;
+            }
+            ok = lane != 0 || ring.put(it, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+          }
+          at += cost;
+          if (at >= x1) more = false;
+        }
+        if (!more) break;
+      }
+      if (at >= x1) break;
+      h = p = 0;
+      if (++b == base + 32 && b < c.batch) load(b);
+    }
+    if (lane == 0) {
+      it.begin = -1;
+      if (ok) ring.put(it, abort_flag);
+      parts[blockIdx.x] = info;
+    }
+  }
+};
 #endif
 
 }  // namespace fa

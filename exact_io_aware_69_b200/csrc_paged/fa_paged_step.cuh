@@ -15,7 +15,8 @@
 // the stage): lanes 64-127 of O^T hold products nobody reads.
 //
 // Column q of an item is token q / group and query head q % group of its key head's group,
-// so all query heads that share a key head share one pass over it.
+// so all query heads that share a key head share one pass over it. Columns beyond the
+// item's rows hold whatever lies in shared memory: a column's values meet no other's.
 //
 // Softmax: thread r of a warpgroup owns key r of the tile and 16 or 32 query columns. The
 // reference m of a column moves only when a score exceeds it by more than 2^8; whether
@@ -27,7 +28,8 @@
 // window, or in pages that are not loaded -- are zeroed in shared memory, since 0 times
 // whatever an unwritten row holds need not be 0.
 //
-// Warps: 4 (NQ <= 32) or 8 (NQ = 64) softmax warps, the TMA producer, the MMA issuer.
+// Warps: 4 (NQ <= 32) or 8 (NQ = 64) softmax warps, two TMA producers (Q and K, V), the MMA
+// issuer, the scheduler.
 #pragma once
 
 #include "fa_paged_split.cuh"
@@ -41,7 +43,7 @@ struct StepLayout {
   static constexpr int kGroups = NQ == 64 ? 2 : 1;  // softmax warpgroups
   static constexpr int kCols = NQ / kGroups;        // query columns of a softmax thread
   static constexpr int kSoftmax = 128 * kGroups;
-  static constexpr int kThreads = kSoftmax + 96;
+  static constexpr int kThreads = kSoftmax + 128;
   static constexpr uint32_t kTileBytes = kKeyTile * D * 2;
   static constexpr uint32_t kChunkBytes = kKeyTile * 128;  // 128 rows x 64 values
   static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // V tile, then K tile
@@ -55,9 +57,9 @@ struct StepLayout {
   static constexpr uint32_t kSums = kRed + 4 * NQ * 4;    // [2][column][warp]
   static constexpr uint32_t kRef = kSums + 8 * NQ * 4;    // [column] reference
   static constexpr uint32_t kTok = kRef + NQ * 4;         // [column] token of a column
-  static constexpr uint32_t kBounds = kTok + NQ * 4;
-  static constexpr uint32_t kBar = kBounds + sizeof(Stretch);
-  static constexpr int kNumBars = 2 * kStages + 10;
+  static constexpr uint32_t kItems = kTok + NQ;
+  static constexpr uint32_t kBar = kItems + kItemSlots * sizeof(Item);
+  static constexpr int kNumBars = 2 * kStages + 10 + 2 * kItemSlots;
   static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
   static constexpr uint32_t kAbort = kTmemSlot + 8;
   static constexpr uint32_t kBytes = kAbort + 8 + 1024;
@@ -67,7 +69,8 @@ struct StepLayout {
   // barriers
   static constexpr int bFull = 0, bEmpty = kStages, bQFull = 2 * kStages, bQEmpty = bQFull + 2,
                        bSFull = bQEmpty + 2, bPFull = bSFull + 2,
-                       bDone = bPFull + 2;  // the product of a P buffer has landed
+                       bDone = bPFull + 2,  // the product of a P buffer has landed
+                       bItems = bDone + 2;
 };
 
 // Byte of (row, key) in an NQ-row, 128-byte-swizzled tile of 128 16-bit columns.
@@ -147,9 +150,9 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sbase + Lay::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbort);
-  int* tok = reinterpret_cast<int*>(smem + Lay::kTok);
-  Stretch* bounds = reinterpret_cast<Stretch*>(smem + Lay::kBounds);
-  constexpr int kProducer = Lay::kSoftmax / 32, kMma = kProducer + 2;  // K, V, MMA
+  uint8_t* tok = smem + Lay::kTok;
+  constexpr int kProducer = Lay::kSoftmax / 32, kMma = kProducer + 2,
+                kScheduler = kMma + 1;
 
   dependents_may_launch();
   if (threadIdx.x == 0) {
@@ -164,23 +167,33 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
       mbar_init(bar(Lay::bPFull + b), Lay::kSoftmax);
       mbar_init(bar(Lay::bDone + b), 1);
     }
+    item_ring_init(bar(Lay::bItems), kProducer + 3);
     *abort_flag = 0;
     fence_mbar_init();
+  }
+  if (warp == kScheduler) {
+    dependency_wait();
+    Scheduler<true> schedule(c, max_q, max_q, wl, wr);
+    schedule.locate(least);
+    __syncthreads();
+    ItemRing ring(sbase + Lay::kItems, bar(Lay::bItems));
+    schedule.run(ring, abort_flag, parts);
+    __syncthreads();
+    return;
   }
   if (warp == kMma) {
     tmem_alloc(sbase + Lay::kTmemSlot, Lay::kTmemCols);
     tmem_relinquish();
   }
-  // columns no query fills: zeros, so that their scores are 0 and move nothing
-  for (uint32_t i = threadIdx.x; i < 2 * Lay::kQBytes / 16; i += Lay::kThreads)
-    *reinterpret_cast<uint4*>(smem + Lay::kQ + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-  if (threadIdx.x < NQ) tok[threadIdx.x] = threadIdx.x / group;
-  tc_fence_before();
+  if (threadIdx.x < NQ) tok[threadIdx.x] = static_cast<uint8_t>(threadIdx.x / group);
   dependency_wait();
-  split_bounds<true>(c, max_q, max_q, wl, wr, least, reinterpret_cast<long long*>(smem), bounds);
+  tc_fence_before();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Lay::kTmemSlot);
-  Walk w(c, max_q, max_q, wl, wr, *bounds);
+  ItemRing ring(sbase + Lay::kItems, bar(Lay::bItems));
+  Item w;
+  bool ok = true;
 
   if (warp == kProducer || warp == kProducer + 1) {
     // --------------------------------------- TMA producers: Q and K, V
@@ -194,12 +207,12 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
     const uint32_t q_bytes = static_cast<uint32_t>(group) * max_q * D * 2;
     const uint32_t at = sbase + (is_k ? Lay::kTileBytes : 0);
     int it = 0, item = 0;
-    bool ok = true;
     PageWindow win;
     win.bad = false;
-    for (; w.more && ok; w.next(c, max_q, max_q, wl, wr)) {
+    while (ok && __all_sync(0xffffffffu, ring.get(&w, &ok, abort_flag))) {
+      ring.read(lane == 0);
       if (w.j0 >= w.j1) continue;
-      win.start(c, w.at.b, (w.keys.first + w.j0) * kKeyTile >> c.page_shift, lane);
+      win.start(c, w.b, (w.keys.first + w.j0) * kKeyTile >> c.page_shift, lane);
       if (is_k) {
         const int qb = item & 1;
         ok = item < 2 || mbar_wait(bar(Lay::bQEmpty + qb),
@@ -209,7 +222,7 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
           mbar_expect_tx(bar(Lay::bQFull + qb), q_bytes);
           for (int i = 0; i < D / 64; ++i)
             tma_load_4d(sbase + Lay::kQ + qb * Lay::kQBytes + i * Lay::kQChunk, &tmQ, i * 64, 0,
-                        w.seq.begin, w.at.h, bar(Lay::bQFull + qb));
+                        w.begin, w.h, bar(Lay::bQFull + qb));
         }
         __syncwarp();
         ++item;
@@ -229,17 +242,15 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
                          static_cast<uint32_t>(pages.count * pages.rows) * D * 2);
         __syncwarp();
         load_tile_pages<D>(pages, tile, c.page_shift, win, map, at + st * Lay::kStageBytes,
-                           bar(Lay::bFull + st), nullptr, 0, 0, w.at.h, lane);
+                           bar(Lay::bFull + st), nullptr, 0, 0, w.h, lane);
       }
     }
     if (win.bad) atomicExch(&g_fa_status, kStatusInvalid);
-    if (is_k && lane == 0) write_part_info(c, max_q, max_q, *bounds, parts);
   } else if (warp == kMma) {
     // -------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_f16_f32(kKeyTile, NQ, BF16, false, false);
       constexpr uint32_t id_o = idesc_f16_f32(128, NQ, BF16, true, false);
-      bool ok = true;
       // O^T += V^T P^T of tile t of the CTA's tiles (accumulate: not an item's first)
       auto product = [&](int t, bool accumulate) -> bool {
         const int st = t % S, pb = t & 1;
@@ -259,7 +270,8 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
       };
       int it = 0, item = 0;
       bool last_accumulates = false;
-      for (; w.more && ok; w.next(c, max_q, max_q, wl, wr)) {
+      while (ok && ring.get(&w, &ok, abort_flag)) {
+        ring.read(true);
         if (w.j0 >= w.j1) continue;
         const int qb = item & 1;
         ok = mbar_wait(bar(Lay::bQFull + qb), static_cast<uint32_t>(item >> 1) & 1, abort_flag);
@@ -298,13 +310,17 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
     const int gbar = 1 + wg;
     // a column that has seen no key: below every finite score, and -inf - kNone = -inf
     constexpr float kNone = -3.402823466e38f;
-    bool ok = true;
     int it = 0;
-    for (; w.more && ok; w.next(c, max_q, max_q, wl, wr)) {
-      const int cols = min(C, w.seq.n * group - q0);  // of this warpgroup, at least 1 in group 0
-      const int off = w.seq.nk - w.seq.n;
+    while (true) {
+      const bool more = ring.get(&w, &ok, abort_flag);
+      __syncwarp();
+      // all of the group leave together; and the last item's sums have been read
+      if (!named_bar_and(gbar, 128, more)) break;
+      ring.read(lane == 0);
+      const int cols = min(C, w.n * group - q0);  // of this warpgroup, at least 1 in group 0
+      const int off = w.nk - w.n;
       // keys that every row sees
-      const int all_lo = w.seq.n - 1 + off - wl, all_hi = min(w.seq.nk - 1, off + wr);
+      const int all_lo = w.n - 1 + off - wl, all_hi = min(w.nk - 1, off + wr);
       float m[C], l[C], l_o[C];
 #pragma unroll
       for (int q = 0; q < C; ++q) {
@@ -331,7 +347,7 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
             for (int q = 0; q < C; ++q) {
               if ((q & 3) == 0 && q >= cols) break;
               const int mid = tok[q0 + q] + off;
-              if (key > min(w.seq.nk - 1, mid + wr) || key < mid - wl) s[q] = -INFINITY;
+              if (key > min(w.nk - 1, mid + wr) || key < mid - wl) s[q] = -INFINITY;
             }
             if (wg == 0 && (key < w.keys.lo || key > w.keys.hi)) {
               const uint32_t v = sbase + (it % S) * Lay::kStageBytes + r * 128;
@@ -457,8 +473,8 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
           const float val = e > 0.f ? __fdividef(__uint_as_float(o[k]), e) : 0.f;
           if (whole) {
             const int tq = tok[q0 + q];
-            const int head = w.at.h * group + q0 + q - tq * group;
-            O[(w.seq.begin + tq) * so.sn + head * so.sh + r] =
+            const int head = w.h * group + q0 + q - tq * group;
+            O[(w.begin + tq) * so.sn + head * so.sh + r] =
                 static_cast<uint16_t>(pack2<BF16>(val, 0.f) & 0xFFFFu);
           } else {
             Opart[(slot * NQ + q0 + q) * D + r] = val;
@@ -472,15 +488,14 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
         const float L2 = a > 0.f ? refs[r] + log2f(a) : -INFINITY;
         if (whole) {
           const int tq = tok[q0 + r];
-          const int head = w.at.h * group + q0 + r - tq * group;
-          L[static_cast<long>(head) * c.tokens + w.seq.begin + tq] =
+          const int head = w.h * group + q0 + r - tq * group;
+          L[static_cast<long>(head) * c.tokens + w.begin + tq] =
               L2 * 0.69314718055994530942f;
         } else {
           Lpart[slot * NQ + q0 + r] = L2;
         }
       }
       tc_fence_before();
-      named_bar_sync(gbar, 128);  // the sums are read before the next item's are written
     }
   }
 
