@@ -256,116 +256,168 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_f16_f32(kKeyTile, kKeyTile, BF16, false, false);
       constexpr uint32_t idesc_o = idesc_f16_f32(kKeyTile, D, BF16, false, true);
-      int ks = 0, vs = 0, item = 0;
-      uint32_t kphase = 0, vphase = 0;
-      uint32_t pphase[2] = {0, 0};
-      // the product that query tile g still owes for the previous tile: 0 none, 1 an
-      // item's first (O is overwritten), 2 a later one; + 4: the item's last
-      int owed[2] = {0, 0};
-      auto product = [&](int g, bool wait_v) -> bool {
-        if (!mbar_wait(bar((kSplitPV ? Lay::bPHalf : Lay::bPFull) + g), pphase[g], abort_flag))
-          return false;
-        if (wait_v && !mbar_wait(bar(Lay::bVFull + vs), vphase, abort_flag)) return false;
-        tc_fence_after();
-        const uint64_t dv =
-            sdesc_sw128(sbase + Lay::kV + vs * Lay::kTileBytes, Lay::kChunkBytes, 1024);
-        const uint32_t a_p = tmem + Lay::tS + g * 128;  // P packed in 64 columns
-        const uint32_t d_o = tmem + Lay::tO + g * D;
-        const bool accumulate = (owed[g] & 3) == 2;
-#pragma unroll
-        for (int k = 0; k < kKeyTile / 32; ++k)
-          mma_ts(d_o, a_p + k * 8, sdesc_step(dv, k * 2048), idesc_o,
-                 (accumulate || k > 0) ? 1u : 0u);
-        if (kSplitPV) {
-          if (!mbar_wait(bar(Lay::bPFull + g), pphase[g], abort_flag)) return false;
-          tc_fence_after();
+      // A tile's turns: the product that query tile 0 owes, 0's scores of this tile, the same
+      // for 1. Where both owe one and both see the tile -- all but an item's edges -- they
+      // are laid out straight; otherwise one body with a run-time g serves every case, since
+      // copies for each made this warp's code 16 KB, which the softmax warps' and it kept
+      // pushing out of the instruction cache, at three times the cost for all code that
+      // runs once an item. (The run-time body alone costs the straight path 12 %.)
+      int ks = 0, item = 0;
+      uint32_t kphase = 0, pphase0 = 0, pphase1 = 0;
+      // what g owes: 0 nothing, else 1 (an item's first product: O is overwritten) or 2, + 4
+      // for the item's last, + 8 times the V tile's index among the CTA's
+      uint32_t owed0 = 0, owed1 = 0;
+      uint32_t vi = 0;  // V tiles before this one
+      bool more = true;
+      while (ok && more) {
+        more = ring.get(&w, &ok, abort_flag);
+        if (!ok) break;
+        if (more) {
+          ring.read(true);
+          if (w.j0 >= w.j1) continue;
         }
-#pragma unroll
-        for (int k = kKeyTile / 32; k < kKeyTile / 16; ++k)
-          mma_ts(d_o, a_p + k * 8, sdesc_step(dv, k * 2048), idesc_o, 1u);
-        pphase[g] ^= 1;
-        if (owed[g] & 4) mma_commit(bar(Lay::bODone + g));
-        owed[g] = 0;
-        return true;
-      };
-      bool v_owed = false;  // the previous tile's V stage is to be released
-      while (ok && ring.get(&w, &ok, abort_flag)) {
-        ring.read(true);
-        if (w.j0 >= w.j1) continue;
         const ChunkTiles t(w, tpt, wl, wr);
-        bool q_waited = false;
-        for (int tile = t.first; ok && tile < t.last; ++tile) {
-          bool v_waited = false, k_waited = false;
-          auto owing = [&](int g) {
-            if (ok && owed[g]) {
-              ok = product(g, !v_waited);
-              v_waited = true;
-            }
-          };
-          auto scores = [&](int g) {
-            if (!ok || !t.in(g, tile)) return;
-            if (!q_waited) {
-              ok = mbar_wait(bar(Lay::bQFull), static_cast<uint32_t>(item) & 1, abort_flag);
-              q_waited = true;
-            }
-            if (ok && !k_waited) {
-              ok = mbar_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
-              k_waited = true;
-            }
-            if (!ok) return;
-            tc_fence_after();
-            const uint64_t dq =
-                sdesc_sw128(sbase + Lay::kQ + (t.one ? 0 : g) * Lay::kTileBytes, 16, 1024);
+        // after the last item, one turn for the products that are owed
+        const int last = more ? t.last : t.first + 1;
+        for (int tile = t.first; ok && tile < last; ++tile) {
+          if (more && !t.one && owed0 != 0 && owed1 != 0 && t.in(0, tile) && t.in(1, tile) &&
+              tile > t.first) {
+            const uint32_t v = owed0 >> 3;
+            const uint32_t vs = v % kChunkVStages;
+            const uint64_t dv =
+                sdesc_sw128(sbase + Lay::kV + vs * Lay::kTileBytes, Lay::kChunkBytes, 1024);
             const uint64_t dk = sdesc_sw128(sbase + Lay::kK + ks * Lay::kTileBytes, 16, 1024);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t koff = (k >> 2) * Lay::kChunkBytes + (k & 3) * 32;
-              mma_ss(tmem + Lay::tS + g * 128, sdesc_step(dq, koff), sdesc_step(dk, koff), idesc_s,
-                     k > 0 ? 1u : 0u);
+            for (int g = 0; g < 2; ++g) {
+              const uint32_t what = g ? owed1 : owed0;
+              const uint32_t parity = g ? pphase1 : pphase0;
+              const uint32_t d_s = tmem + Lay::tS + g * 128, d_o = tmem + Lay::tO + g * D;
+              ok = mbar_wait(bar((kSplitPV ? Lay::bPHalf : Lay::bPFull) + g), parity,
+                             abort_flag) &&
+                   (g == 1 || mbar_wait(bar(Lay::bVFull + vs), (v / kChunkVStages) & 1,
+                                        abort_flag));
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t accumulate = (what & 3u) == 2u ? 1u : 0u;
+#pragma unroll
+              for (int k = 0; k < kKeyTile / 32; ++k)
+                mma_ts(d_o, d_s + k * 8, sdesc_step(dv, k * 2048), idesc_o,
+                       k > 0 ? 1u : accumulate);
+              if (kSplitPV) {
+                ok = mbar_wait(bar(Lay::bPFull + g), parity, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+              }
+#pragma unroll
+              for (int k = kKeyTile / 32; k < kKeyTile / 16; ++k)
+                mma_ts(d_o, d_s + k * 8, sdesc_step(dv, k * 2048), idesc_o, 1u);
+              if (g == 0) {
+                ok = mbar_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              const uint64_t dq = sdesc_sw128(sbase + Lay::kQ + g * Lay::kTileBytes, 16, 1024);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t koff = (k >> 2) * Lay::kChunkBytes + (k & 3) * 32;
+                mma_ss(d_s, sdesc_step(dq, koff), sdesc_step(dk, koff), idesc_s, k > 0 ? 1u : 0u);
+              }
+              mma_commit(bar(Lay::bSFull + g));
             }
-            mma_commit(bar(Lay::bSFull + g));
-            owed[g] = (tile == (g ? t.lo[1] : t.lo[0]) ? 1 : 2) + (t.last_of(g, tile) ? 4 : 0);
-          };
-          // the previous tile's products and this one's scores; with one query tile the
-          // scores (of the other group than the product) go first
-          const int turns = t.one && tile > t.first;
-          if (turns && ((tile - t.first) & 1)) {
-            scores(1);
-            owing(0);
-          } else if (turns) {
-            scores(0);
-            owing(1);
-          } else {
-            owing(0);
-            scores(0);
-            owing(1);
-            scores(1);
+            if (!ok) break;
+            mma_commit(bar(Lay::bVEmpty + vs));
+            mma_commit(bar(Lay::bKEmpty + ks));
+            pphase0 ^= 1;
+            pphase1 ^= 1;
+            owed0 = 2u + (t.last_of(0, tile) ? 4u : 0u) + 8u * vi;
+            owed1 = 2u + (t.last_of(1, tile) ? 4u : 0u) + 8u * vi;
+            ++vi;
+            if (++ks == kChunkKStages) {
+              ks = 0;
+              kphase ^= 1;
+            }
+            continue;
           }
-          if (!ok) break;
+          // an item's first tile: both groups (the item before may have left products owed)
+          const bool alone = t.one && tile > t.first;
+          int g = alone ? (tile - t.first) & 1 : 0;
+          bool k_waited = false;
+#pragma unroll 1
+          for (int turns = alone ? 1 : 2; turns > 0; --turns, g ^= 1) {
+            const uint32_t what = g ? owed1 : owed0;
+            const uint32_t d_s = tmem + Lay::tS + g * 128;  // S, and P packed in 64 columns
+            if (what != 0) {
+              const uint32_t parity = g ? pphase1 : pphase0;
+              const uint32_t v = what >> 3;
+              const uint32_t vs = v % kChunkVStages;
+              ok = mbar_wait(bar((kSplitPV ? Lay::bPHalf : Lay::bPFull) + g), parity,
+                             abort_flag) &&
+                   mbar_wait(bar(Lay::bVFull + vs), (v / kChunkVStages) & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dv =
+                  sdesc_sw128(sbase + Lay::kV + vs * Lay::kTileBytes, Lay::kChunkBytes, 1024);
+              const uint32_t d_o = tmem + Lay::tO + g * D;
+              const uint32_t accumulate = (what & 3u) == 2u ? 1u : 0u;
+#pragma unroll
+              for (int k = 0; k < kKeyTile / 32; ++k)
+                mma_ts(d_o, d_s + k * 8, sdesc_step(dv, k * 2048), idesc_o,
+                       k > 0 ? 1u : accumulate);
+              if (kSplitPV) {
+                ok = mbar_wait(bar(Lay::bPFull + g), parity, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+              }
+#pragma unroll
+              for (int k = kKeyTile / 32; k < kKeyTile / 16; ++k)
+                mma_ts(d_o, d_s + k * 8, sdesc_step(dv, k * 2048), idesc_o, 1u);
+              if (what & 4u) mma_commit(bar(Lay::bODone + g));
+              const uint32_t other = g ? owed0 : owed1;
+              if (other == 0 || other >> 3 != v) mma_commit(bar(Lay::bVEmpty + vs));
+              if (g) {
+                pphase1 ^= 1;
+                owed1 = 0;
+              } else {
+                pphase0 ^= 1;
+                owed0 = 0;
+              }
+            }
+            if (more && t.in(g, tile)) {
+              if (tile == t.first)
+                ok = mbar_wait(bar(Lay::bQFull), static_cast<uint32_t>(item) & 1, abort_flag);
+              if (ok && !k_waited) ok = mbar_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
+              if (!ok) break;
+              k_waited = true;
+              tc_fence_after();
+              const uint64_t dq =
+                  sdesc_sw128(sbase + Lay::kQ + (t.one ? 0 : g) * Lay::kTileBytes, 16, 1024);
+              const uint64_t dk = sdesc_sw128(sbase + Lay::kK + ks * Lay::kTileBytes, 16, 1024);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t koff = (k >> 2) * Lay::kChunkBytes + (k & 3) * 32;
+                mma_ss(d_s, sdesc_step(dq, koff), sdesc_step(dk, koff), idesc_s, k > 0 ? 1u : 0u);
+              }
+              mma_commit(bar(Lay::bSFull + g));
+              const uint32_t next = (tile == (g ? t.lo[1] : t.lo[0]) ? 1u : 2u) +
+                                    (t.last_of(g, tile) ? 4u : 0u) + 8u * vi;
+              if (g)
+                owed1 = next;
+              else
+                owed0 = next;
+            }
+          }
+          if (!ok || !more) break;
           mma_commit(bar(Lay::bKEmpty + ks));
+          ++vi;
           if (++ks == kChunkKStages) {
             ks = 0;
             kphase ^= 1;
           }
-          if (v_owed) {
-            mma_commit(bar(Lay::bVEmpty + vs));
-            if (++vs == kChunkVStages) {
-              vs = 0;
-              vphase ^= 1;
-            }
-          }
-          v_owed = true;
         }
-        if (ok) mma_commit(bar(Lay::bQEmpty));
+        if (!ok || !more) break;
+        mma_commit(bar(Lay::bQEmpty));
         ++item;
       }
-      bool v_waited = false;
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        if (ok && owed[g]) {
-          ok = product(g, !v_waited);
-          v_waited = true;
-        }
     }
   } else if (warp < 8) {
     // ----------------------------------------------------------------- softmax
