@@ -162,6 +162,18 @@ bool make_tmap(CUtensorMap* map, const void* ptr, int dtype, const long long (&d
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// The parts' outputs, fp32 rows of d columns, in boxes of 32 columns x 32 rows.
+bool make_part_tmap(CUtensorMap* map, const float* ptr, int d, int rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t size[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(d) * 4};
+  const cuuint32_t box[2] = {32, 32}, step[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(ptr), size, stride, box,
+             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // A stride of 0 over more than one row would alias rows of a tensor map.
 bool steps(long long stride, long long rows) { return rows <= 1 || stride > 0; }
 
@@ -218,13 +230,13 @@ bool make_maps(const AttentionArgs& a, int tokens, CUtensorMap* q, CUtensorMap* 
 
 // Joins the parts of items of up to `rows` rows.
 template <int D, int WPR, bool BF16>
-int launch_merge(const AttentionArgs& a, int rows) {
+int launch_merge(const AttentionArgs& a, int rows, int tile_tokens) {
   constexpr int kRows = fa::kMergeThreads / 32 / WPR;
   const dim3 grid(kGrid, static_cast<unsigned>((rows + kRows - 1) / kRows));
   return launch(fa::fa_paged_merge_kernel<D, WPR, BF16>, grid, fa::kMergeThreads, 0, a.stream,
                 static_cast<const float*>(a.opart()), static_cast<const float*>(a.lpart()),
-                static_cast<const fa::PartInfo*>(a.parts()), a.ws.rows, a.group,
-                static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.c->tokens);
+                static_cast<const fa::PartInfo*>(a.parts()), a.ws.rows, tile_tokens, fa::kKeyTile,
+                a.group, static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.c->tokens);
 }
 
 // A kernel's shared-memory limit, set on every call: it is the current context's.
@@ -249,7 +261,7 @@ int launch_step(const AttentionArgs& a) {
                         view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.opart(),
                         a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kStepLeast,
                         a.scale * kLog2e);
-  return st != FA_OK ? st : launch_merge<D, 8, BF16>(a, a.max_q * a.group);
+  return st != FA_OK ? st : launch_merge<D, 8, BF16>(a, a.max_q * a.group, a.max_q);
 }
 
 // ... and for chunks, whose tiles take longer and whose parts are larger.
@@ -271,12 +283,20 @@ int launch_chunk(const AttentionArgs& a) {
   }
   if (!allow_smem(kern, Lay::kSmem)) return FA_ERR_CUDA;
   CUtensorMap q, k, v;
-  if (!make_maps(a, fa::kKeyTile / a.group, &q, &k, &v)) return FA_ERR_CUDA;
+  const int tpt = fa::kKeyTile / a.group;
+  // a warp's 32 rows of the output, where those are whole tokens (the kernel asks the same)
+  const int out_tokens = 32 % a.group == 0 ? 32 / a.group : 1;
+  CUtensorMap o, part;
+  if (!make_maps(a, tpt, &q, &k, &v) ||
+      !make_tmap(&o, a.O, a.c->dtype, {a.c->d, a.group, a.c->tokens, a.c->heads},
+                 {a.xo.h, a.xo.n, a.xo.h * a.group}, a.group, out_tokens) ||
+      !make_part_tmap(&part, a.opart(), D, 2 * kGrid * a.ws.rows))
+    return FA_ERR_CUDA;
   const int st = launch(kern, dim3(kGrid), fa::kChunkThreads, Lay::kSmem, a.stream, q, k, v,
-                        view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.opart(),
+                        o, part, view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L,
                         a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kChunkLeast,
                         a.scale * kLog2e);
-  return st != FA_OK ? st : launch_merge<D, 1, BF16>(a, fa::kChunkRows);
+  return st != FA_OK ? st : launch_merge<D, 1, BF16>(a, fa::kChunkRows, tpt);
 }
 
 template <int D, bool BF16>

@@ -116,9 +116,11 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     fa_paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK,
-                          const __grid_constant__ CUtensorMap tmV, const PagedView c,
+                          const __grid_constant__ CUtensorMap tmV,
+                          const __grid_constant__ CUtensorMap tmO,
+                          const __grid_constant__ CUtensorMap tmPart, const PagedView c,
                           uint16_t* __restrict__ O, Strides so, float* __restrict__ L,
-                          float* __restrict__ Opart, float* __restrict__ Lpart,
+                          float* __restrict__ Lpart,
                           PartInfo* __restrict__ parts, int group, int max_q, int wl, int wr,
                           int least,
                           float scale_log2) {
@@ -502,9 +504,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             seen &= lo_bit > 31 ? 0u : 0xffffffffu << max(lo_bit, 0);
             if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
             uint32_t x[32];
-            tmem_ld32(lane_base + s_cols + h * 32, x);
-            tmem_wait_ld();
-            reg_fence32(x);
+            if (__any_sync(0xffffffffu, seen != 0)) {
+              tmem_ld32(lane_base + s_cols + h * 32, x);
+              tmem_wait_ld();
+              reg_fence32(x);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = 0u;
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1 ? x[i] : 0xff800000u;
             tmem_st32(lane_base + s_cols + h * 32, x);
@@ -625,21 +632,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       // O / l_o: a thread holds a row, a store wants rows' neighbours side by side, so 128
       // bytes of each row (64 columns, or 32 of a part in fp32) at a time go through the
-      // warp's 4 KB of shared memory, 16-byte pieces swizzled by row, and leave as four
-      // rows of 128 bytes an instruction. (Straight from the rows' threads an item's store
-      // took 3000 to 8000 cycles, this one about 900.)
+      // warp's 4 KB of shared memory, 128-byte-swizzled, and leave in one TMA store (of a
+      // part's rows, or of whole tokens when 32 rows are that) or, at a sequence's ragged end,
+      // as four rows an instruction. (Straight from the rows' threads an item's store took
+      // 3000 to 8000 cycles.)
       if (ok && busy && !(one && g == 1)) {
         const bool whole = w.j0 == 0 && w.j1 == w.keys.count;
         const bool other_some = one && first + 1 < w.keys.first + w.j1;
         const int rows = min(tpt, w.n - tok0) * group;  // of the query tile
         const int row0 = quarter * 32;
-        const long slot_row = (w.j0 > 0 ? 2L * blockIdx.x : 2L * blockIdx.x + 1) * kChunkRows +
-                              (one ? 0 : g) * tpt * group;
+        const int tok_row0 = row0 * by_group >> 16;  // token of the warp's first row
+        const int slot_row = (w.j0 > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * kChunkRows +
+                             (one ? 0 : g * kKeyTile);
+        const bool by_tma = !whole || (32 % group == 0 && row0 + 32 <= rows);
         const uint32_t stage = sbase + Lay::kOut + warp * 4096;
-        const int piece = lane & 7;
-                uint16_t* out = O + static_cast<long>(w.begin + tok0) * so.sn +
-                        static_cast<long>(w.h) * group * so.sh + piece * 8;
-        float* part = Opart + (slot_row + row0 + (lane >> 3)) * D + piece * 4;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
           float x[32];
@@ -661,6 +667,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o[e]), inv_other, x[e]);
           }
+          // the bytes before have left (they did so at once, except by TMA)
+          if (lane == 0 && by_tma && (!whole || (i & 32) == 0)) bulk_wait_read_all();
+          __syncwarp();
           if (whole) {  // half of the row's 128 bytes; they leave after the second half
             const int half = (i >> 5) & 1;
 #pragma unroll
@@ -681,31 +690,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                            "f"(x[4 * e]), "f"(x[4 * e + 1]), "f"(x[4 * e + 2]), "f"(x[4 * e + 3])
                            : "memory");
           }
-          __syncwarp();
-          uint4 y[8];  // row 4 e + lane / 8 of the warp, all loaded before the first leaves
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int sr = 4 * e + (lane >> 3);
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(y[e].x), "=r"(y[e].y), "=r"(y[e].z), "=r"(y[e].w)
-                         : "r"(stage + sr * 128 + ((piece ^ (sr & 7)) << 4))
-                         : "memory");
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int row = row0 + 4 * e + (lane >> 3);  // of the query tile
-            if (row < rows) {
-              if (whole) {
+          if (by_tma) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (whole)
+                tma_store_4d(&tmO, stage, i - 32, 0, w.begin + tok0 + tok_row0, w.h);
+              else
+                tma_store_2d(&tmPart, stage, i, slot_row + row0);
+              bulk_commit();
+            }
+          } else {
+            __syncwarp();
+#pragma unroll 1
+            for (int e = lane >> 3; e < 32; e += 4) {
+              const int row = row0 + e;
+              uint4 y;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                           : "r"(stage + e * 128 + (((lane & 7) ^ (e & 7)) << 4))
+                           : "memory");
+              if (row < rows) {
                 const int t = row * by_group >> 16;
-                *reinterpret_cast<uint4*>(out + t * so.sn + (row - t * group) * so.sh + (i - 32)) =
-                    y[e];
-              } else {
-                *reinterpret_cast<uint4*>(part + 4 * e * D + i) = y[e];
+                *reinterpret_cast<uint4*>(O + static_cast<long>(w.begin + tok0 + t) * so.sn +
+                                          (w.h * group + row - t * group) * so.sh + (i - 32) +
+                                          (lane & 7) * 8) = y;
               }
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
+        // what left by TMA has to be out before the CTA ends, and read before it is reused
+        if (lane == 0 && by_tma) bulk_wait_all();
         if (r < rows) {
           if (whole)
             L[static_cast<long>(w.h * group + head_in) * c.tokens + w.begin + tok0 + tr] =

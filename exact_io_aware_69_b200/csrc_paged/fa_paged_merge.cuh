@@ -4,6 +4,9 @@
 // the recurrence of the online softmax applied to whole parts, in the order of the CTAs
 // that computed them.
 //
+// A part's rows come in tiles of `tile_tokens` tokens, `tile_rows` rows apart; row q of
+// token t of a tile is t * group + q.
+//
 // Block (c, y) serves rows of the item whose first part is CTA c's slot 2 c + 1; it ends at
 // once when there is none. WPR warps share a row's parts: eight for a decode step, whose
 // few rows may have up to a part per SM, one for chunks, whose many rows have few. Bound
@@ -21,8 +24,8 @@ static_assert(kMergeThreads >= kSplitGrid, "one thread per CTA of the split");
 template <int D, int WPR, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads)
     fa_paged_merge_kernel(const float* __restrict__ Opart, const float* __restrict__ Lpart,
-                          const PartInfo* __restrict__ parts, int rows_per_slot, int group,
-                          uint16_t* __restrict__ O, Strides so, float* __restrict__ L,
+                          const PartInfo* __restrict__ parts, int rows_per_slot, int tile_tokens,
+                          int tile_rows, int group, uint16_t* __restrict__ O, Strides so, float* __restrict__ L,
                           int tokens) {
   constexpr int CPL = D / 32;
   constexpr int kRows = kMergeThreads / 32 / WPR;  // rows of a block
@@ -47,8 +50,12 @@ __global__ void __launch_bounds__(kMergeThreads)
   float M = -INFINITY, tot = 0.f, o[CPL];
 #pragma unroll
   for (int i = 0; i < CPL; ++i) o[i] = 0.f;
+  const int t = r / group;
+  const int q = r - t * group;
+  const int tile = t / tile_tokens;
+  const int in_slot = tile * tile_rows + (t - tile * tile_tokens) * group + q;
   auto row_of = [&](int s) -> long {
-    return (s == 0 ? 2L * c + 1 : 2L * (c + s)) * rows_per_slot + r;
+    return (s == 0 ? 2L * c + 1 : 2L * (c + s)) * rows_per_slot + in_slot;
   };
   if (live) {
     for (int s = w + lane * WPR; s < n; s += 32 * WPR) M = fmaxf(M, Lpart[row_of(s)]);
@@ -102,8 +109,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
   if (!live) return;
   const float inv = tot > 0.f ? 1.f / tot : 0.f;
-  const int t = r / group;
-  const int head = info.head * group + (r - t * group);
+  const int head = info.head * group + q;
   uint16_t* dst = O + (info.token0 + t) * so.sn + head * so.sh + lane * CPL;
   if constexpr (CPL == 4)
     *reinterpret_cast<uint2*>(dst) =
