@@ -57,12 +57,11 @@ int check_rotation(int d, int rot_dim, float magnitude, const double* freqs) {
   return rot_dim % 16 == 0 ? FA_OK : FA_ERR_UNSUPPORTED;
 }
 
-// Tokens of a block: one while that gives every SM at most a block or two (a token's rows
-// then finish soonest), up to eight for long inputs, whose rows keep a thread's angles in
-// registers for longer.
+// Tokens of a block: one while that gives every SM at most a few blocks (a token's rows
+// then finish soonest), more for long inputs.
 int rope_tokens_per_block(long rows, int groups) {
   int t = 1;
-  while (t < fa::kRopeMaxTokens && rows / (2 * t) >= 148 * 2 &&
+  while (t < fa::kRopeMaxTokens && rows / (2 * t) >= 148 * 4 &&
          fa::kRopeThreads / groups / (2 * t) >= 1)
     t *= 2;
   return t;
@@ -71,6 +70,8 @@ int rope_tokens_per_block(long rows, int groups) {
 template <bool PAGED>
 int launch_rope(fa::RopeArgs& a, bool interleaved, int dtype, cudaStream_t stream) {
   a.tokens_per_block = rope_tokens_per_block(a.rows, a.d / 16);
+  const fa::RopeRows& most = a.q.heads > 0 ? a.q : a.k;
+  a.tokens_first = most.ss.sn < most.ss.sh;
   const long blocks = (a.rows + a.tokens_per_block - 1) / a.tokens_per_block;
   if (blocks >= (1L << 31)) return FA_ERR_UNSUPPORTED;
   const size_t smem = static_cast<size_t>(a.tokens_per_block) * a.rot * sizeof(float);

@@ -184,9 +184,12 @@ struct Scheduler {
   // Cost per key head of this lane's sequence.
   __device__ __forceinline__ unsigned seq_cost() const {
     if (ONE_ITEM) return seq.n > 0 ? cost_of(0, seq.n, seq.nk) : 0;
+    // short ones each by its lane, long ones by the warp, one after the other (a lane's turn
+    // is ~60 cycles, a sequence's ~400)
     unsigned sum = 0;
-    // sequence by sequence, its items over the lanes
-    for (unsigned todo = __ballot_sync(0xffffffffu, seq.n > 0); todo; todo &= todo - 1) {
+    const bool own = seq.n <= 16 * tpi;
+    for (int i = 0; own && i * tpi < seq.n; ++i) sum += cost_of(i, seq.n, seq.nk);
+    for (unsigned todo = __ballot_sync(0xffffffffu, !own); todo; todo &= todo - 1) {
       const int l = __ffs(todo) - 1;
       const int n = __shfl_sync(0xffffffffu, seq.n, l), nk = __shfl_sync(0xffffffffu, seq.nk, l);
       unsigned part = 0;

@@ -8,21 +8,27 @@
 // result is rounded once to 16 bits.
 //
 // The pass is bound by HBM: every element is read and written once. So a block takes a few
-// tokens, computes their rot_dim / 2 sines and cosines once into shared memory (a token's
+// tokens and computes their rot_dim / 2 sines and cosines once into shared memory (a token's
 // angles serve all its heads; per thread and head they would cost more instructions than
-// the rotation), and its threads then stream rows: a thread owns 16 columns of a row as two
-// 16-byte vectors (the two halves of eight pairs in the half form, 16 neighbours in the
-// interleaved form, or 16 columns that are copied) and keeps their angles in registers over
-// the heads of its token. kRopeRows rows are loaded before the first is stored.
+// the rotation); its threads then stream rows: a thread owns two 16-byte vectors of a row, half the rotated (or half the copied) columns
+// apart, so that in the half form it holds both columns of its pairs, neighbouring threads
+// hold neighbouring vectors in both forms, and every store covers whole sectors; it keeps
+// its angles in registers over the heads of its token. Threads of a warp run over the
+// heads of a token or over tokens, whichever lie closer together in memory.
+//
+// Small blocks and two rows in flight per thread keep 2048 threads on an SM, which is what
+// carries the bandwidth: 2 x 8192 tokens of 32 + 8 heads, d 128, bf16 (336 MB) take 55.4 us
+// (6.06 TB/s, 0.93 of the copy rate); 256 threads with 2 / 4 / 5 rows 56.2 / 57.6 / 65.2,
+// loading the first rows before the angles are there 57.7 to 65.
 #pragma once
 
 #include "fa_paged_common.cuh"
 
 namespace fa {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = 4;          // rows in flight per thread
-constexpr int kRopeMaxTokens = 8;     // tokens of a block
+constexpr int kRopeThreads = 128;
+constexpr int kRopeRows = 2;          // rows in flight per thread
+constexpr int kRopeMaxTokens = 4;     // tokens of a block
 constexpr int kRopeMaxDim = 1024;
 
 struct RopeRows {
@@ -42,6 +48,7 @@ struct RopeArgs {
   int N;                  // rows per batch (rope), packed rows (append: one batch)
   long rows;              // B * N
   int tokens_per_block;
+  bool tokens_first;      // neighbouring threads take neighbouring tokens, not heads
   PagedView cache;        // append only; its pages are the destination of k and v
 };
 
@@ -92,23 +99,51 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a,
   const long t0 = static_cast<long>(blockIdx.x) * tpb;
   const int nt = static_cast<int>(min(static_cast<long>(tpb), a.rows - t0));
   const int half = a.rot / 2;
-  float* cosines = rope_smem;
-  float* sines = rope_smem + tpb * half;
 
+  // thread = (token, row lane, pair of vectors), vectors fastest
+  const int groups = a.d / 16;
+  const int rlanes = kRopeThreads / groups / tpb;  // threads' rows of one token per pass
+  const int g = threadIdx.x % groups;
+  const int rest = threadIdx.x / groups;
+  const int ti = a.tokens_first ? rest % tpb : rest / rlanes;
+  const int rl = a.tokens_first ? rest / tpb : rest - ti * rlanes;
+  const bool active = ti < nt && rl < rlanes;
+  const long t = t0 + ti;
+  const long b = PAGED ? 0 : t / a.N;
+  const long n = PAGED ? t : t - b * a.N;
+  const bool turns = g < a.rot / 16;
+  // the columns of the thread's two vectors
+  const int c0 = turns ? 8 * g : a.rot + 8 * (g - a.rot / 16);
+  const int c1 = c0 + (turns ? half : (a.d - a.rot) / 2);
+  const int nq = a.q.heads, nk = nq + a.k.heads, total = nk + a.v.heads;
+  uint4 x[kRopeRows], y[kRopeRows];
+  auto fetch = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < kRopeRows; ++u) {
+      const int r = r0 + u * rlanes;
+      if (r < total) {
+        const RopeRows& rows = r < nq ? a.q : r < nk ? a.k : a.v;
+        const int h = r < nq ? r : r < nk ? r - nq : r - nk;
+        const uint16_t* src = rows.src + b * rows.ss.sb + h * rows.ss.sh + n * rows.ss.sn;
+        x[u] = *reinterpret_cast<const uint4*>(src + c0);
+        y[u] = *reinterpret_cast<const uint4*>(src + c1);
+      }
+    }
+  };
   if constexpr (PAGED) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = warp; i < nt; i += kRopeThreads / 32) {
       const PagedView& c = a.cache;
-      const int t = static_cast<int>(t0) + i;
-      const int b = owner_of(c.cu_q, c.batch, t, lane);
+      const int tok = static_cast<int>(t0) + i;
+      const int seq = owner_of(c.cu_q, c.batch, tok, lane);
       if (lane == 0) {
         int owner = -1, page = -1, row = 0, pos = 0;
-        if (b >= 0 && t < c.cu_q[c.batch]) {
-          const SeqInfo s = seq_info(c, b, c.tokens);
-          pos = s.nk - s.n + (t - s.begin);
-          if (s.ok && s.n <= s.nk && t < s.begin + s.n) {
-            owner = b;
-            page = c.table[static_cast<long>(b) * c.table_row + (pos >> c.page_shift)];
+        if (seq >= 0 && tok < c.cu_q[c.batch]) {
+          const SeqInfo s = seq_info(c, seq, c.tokens);
+          pos = s.nk - s.n + (tok - s.begin);
+          if (s.ok && s.n <= s.nk && tok < s.begin + s.n) {
+            owner = seq;
+            page = c.table[static_cast<long>(seq) * c.table_row + (pos >> c.page_shift)];
             row = pos & ((1 << c.page_shift) - 1);
             if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_pages)) page = -1;
           }
@@ -117,18 +152,20 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a,
         s_owner[i] = owner;
         s_page[i] = page;
         s_row[i] = row;
-        s_pos[i] = a.positions != nullptr && owner >= 0 ? a.positions[t] : pos;
+        s_pos[i] = a.positions != nullptr && owner >= 0 ? a.positions[tok] : pos;
       }
     }
   } else {
     if (threadIdx.x < nt) {
-      const long t = t0 + threadIdx.x;
-      const long b = t / a.N;
-      const int n = static_cast<int>(t - b * a.N);
-      s_pos[threadIdx.x] = a.positions != nullptr ? a.positions[b * a.pos_row + n] : n;
+      const long tok = t0 + threadIdx.x;
+      const long bb = tok / a.N;
+      const int nn = static_cast<int>(tok - bb * a.N);
+      s_pos[threadIdx.x] = a.positions != nullptr ? a.positions[bb * a.pos_row + nn] : nn;
     }
   }
   __syncthreads();
+  float* cosines = rope_smem;
+  float* sines = rope_smem + tpb * half;
   for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
     float s, c;
     sincos_of(s_pos[i / half], a.freqs[i % half], &s, &c);
@@ -136,59 +173,39 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a,
     sines[i] = s * a.magnitude * a.sign;
   }
   __syncthreads();
+  if (!active || (PAGED && s_owner[ti] < 0)) return;
 
-  // thread = (token, row lane, group of 16 columns), groups fastest
-  const int groups = a.d / 16;
-  const int rlanes = kRopeThreads / groups / tpb;  // threads' rows of one token per pass
-  const int g = threadIdx.x % groups;
-  const int rest = threadIdx.x / groups;
-  const int ti = rest / rlanes;
-  const int rl = rest - ti * rlanes;
-  if (ti >= nt) return;
-  if (PAGED && s_owner[ti] < 0) return;
-  const long t = t0 + ti;
-  const long b = PAGED ? 0 : t / a.N;
-  const long n = PAGED ? t : t - b * a.N;
-  const bool turns = g < a.rot / 16;
-  // first column of the group's two vectors
-  const int c0 = !turns || interleaved ? 16 * g : 8 * g;
-  const int c1 = !turns || interleaved ? c0 + 8 : c0 + half;
   float cs[8], sn[8];
   if (turns) {
+    // pairs of the first vector and of the second: the same eight, or four and four
+    const float* c = cosines + ti * half + (interleaved ? 4 * g : 8 * g);
+    const float* s = sines + ti * half + (interleaved ? 4 * g : 8 * g);
+    const int second = interleaved ? half / 2 : 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      cs[i] = cosines[ti * half + 8 * g + i];
-      sn[i] = sines[ti * half + 8 * g + i];
+    for (int i = 0; i < 4; ++i) {
+      cs[i] = c[i];
+      sn[i] = s[i];
+      cs[4 + i] = c[second + i];
+      sn[4 + i] = s[second + i];
     }
   }
-  const int nq = a.q.heads, nk = nq + a.k.heads, total = nk + a.v.heads;
   // rows of K and V whose page is not valid are not written
   const int last = PAGED && s_page[ti] < 0 ? nq : total;
   for (int r0 = rl; r0 < last; r0 += kRopeRows * rlanes) {
-    uint4 x[kRopeRows], y[kRopeRows];
-    uint16_t* dst[kRopeRows];
-#pragma unroll
-    for (int u = 0; u < kRopeRows; ++u) {
-      const int r = r0 + u * rlanes;
-      if (r < last) {
-        const RopeRows& rows = r < nq ? a.q : r < nk ? a.k : a.v;
-        const int h = r < nq ? r : r < nk ? r - nq : r - nk;
-        const uint16_t* src = rows.src + b * rows.ss.sb + h * rows.ss.sh + n * rows.ss.sn;
-        x[u] = *reinterpret_cast<const uint4*>(src + c0);
-        y[u] = *reinterpret_cast<const uint4*>(src + c1);
-        // append: K and V rows go to row s_row of page s_page (sb: the page stride)
-        dst[u] = PAGED && r >= nq ? rows.dst + s_page[ti] * rows.sd.sb + h * rows.sd.sh +
-                                        s_row[ti] * rows.sd.sn
-                                  : rows.dst + b * rows.sd.sb + h * rows.sd.sh + n * rows.sd.sn;
-      }
-    }
+    fetch(r0);
 #pragma unroll
     for (int u = 0; u < kRopeRows; ++u) {
       const int r = r0 + u * rlanes;
       if (r < last) {
         if (turns && r < nk) rotate16<BF16>(x[u], y[u], cs, sn, interleaved);
-        *reinterpret_cast<uint4*>(dst[u] + c0) = x[u];
-        *reinterpret_cast<uint4*>(dst[u] + c1) = y[u];
+        const RopeRows& rows = r < nq ? a.q : r < nk ? a.k : a.v;
+        const int h = r < nq ? r : r < nk ? r - nq : r - nk;
+        // append: K and V rows go to row s_row of page s_page (sb: the page stride)
+        uint16_t* dst = PAGED && r >= nq ? rows.dst + s_page[ti] * rows.sd.sb + h * rows.sd.sh +
+                                               s_row[ti] * rows.sd.sn
+                                         : rows.dst + b * rows.sd.sb + h * rows.sd.sh + n * rows.sd.sn;
+        *reinterpret_cast<uint4*>(dst + c0) = x[u];
+        *reinterpret_cast<uint4*>(dst + c1) = y[u];
       }
     }
   }

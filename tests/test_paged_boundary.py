@@ -178,7 +178,7 @@ def test_workspace_size(lib):
 
 # Threads per block of every kernel the library launches.
 # (fa_paged_step_kernel: 192 up to 32 query columns, 320 for 64)
-BLOCK_THREADS = {"fa_rope_kernel": 256, "fa_paged_step_kernel": 192, "fa_paged_merge_kernel": 256,
+BLOCK_THREADS = {"fa_rope_kernel": 128, "fa_paged_step_kernel": 192, "fa_paged_merge_kernel": 256,
                  "fa_paged_chunk_kernel": 384}
 
 
