@@ -229,13 +229,13 @@ bool make_maps(const AttentionArgs& a, int tokens, CUtensorMap* q, CUtensorMap* 
                    {c.v_row, c.v_head, c.v_page}, rows, 1);
 }
 
-// Joins the parts of items of up to `rows` rows.
-template <int D, int WPR, bool BF16>
-int launch_merge(const AttentionArgs& a, int rows, int tile_tokens) {
-  constexpr int kRows = fa::kMergeThreads / 32 / WPR;
-  const dim3 grid(kGrid, static_cast<unsigned>((rows + kRows - 1) / kRows));
-  return launch(fa::fa_paged_merge_kernel<D, WPR, BF16>, grid, fa::kMergeThreads, 0, a.stream,
-                static_cast<const float*>(a.opart()), static_cast<const float*>(a.lpart()),
+// Joins the parts of items whose query tiles have `tile_tokens` tokens, with `per_sm` blocks
+// for each SM.
+template <int D, bool BF16>
+int launch_merge(const AttentionArgs& a, int tile_tokens, unsigned per_sm) {
+  return launch(fa::fa_paged_merge_kernel<D, BF16>, dim3(kGrid * per_sm), fa::kMergeThreads, 0,
+                a.stream, static_cast<const float*>(a.opart()),
+                static_cast<const float*>(a.lpart()),
                 static_cast<const fa::PartInfo*>(a.parts()), a.ws.rows, tile_tokens, fa::kKeyTile,
                 a.group, static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.c->tokens);
 }
@@ -262,7 +262,7 @@ int launch_step(const AttentionArgs& a) {
                         view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.opart(),
                         a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kStepLeast,
                         a.scale * kLog2e);
-  return st != FA_OK ? st : launch_merge<D, 8, BF16>(a, a.max_q * a.group, a.max_q);
+  return st != FA_OK ? st : launch_merge<D, BF16>(a, a.max_q, 2);
 }
 
 // ... and for chunks, whose tiles take longer and whose parts are larger.
@@ -297,7 +297,7 @@ int launch_chunk(const AttentionArgs& a) {
                         o, part, view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L,
                         a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kChunkLeast,
                         a.scale * kLog2e);
-  return st != FA_OK ? st : launch_merge<D, 1, BF16>(a, fa::kChunkRows, tpt);
+  return st != FA_OK ? st : launch_merge<D, BF16>(a, tpt, 8);
 }
 
 template <int D, bool BF16>

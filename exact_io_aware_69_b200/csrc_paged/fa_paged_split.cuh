@@ -23,9 +23,9 @@
 namespace fa {
 
 constexpr int kKeyTile = 128;
-// One tile's time, about: an item's first scores wait for its first keys, and its last
+// About two tiles' time: an item's first scores wait for its first keys, and its last
 // product is followed by the sums and the store.
-constexpr int kItemCost = 1;
+constexpr int kItemCost = 2;
 
 struct KeyRange {
   int lo, hi;        // keys that some row of the item sees (lo > hi: none)
@@ -50,16 +50,13 @@ __host__ __device__ inline int item_cost(const KeyRange& r) { return r.count + k
 // CTAs of an attention launch: one per SM of a B200. A fixed count keeps the split the
 // same everywhere, and divisions by it are multiplications.
 constexpr int kSplitGrid = 148;
-// A CTA's share of cost W (which the host keeps below kMaxCost, so that 32 bits hold every
-// sum here): an even part of it, at least `least`.
+// Start of CTA c's stretch of cost W: even stretches, but none shorter than `least`. (The
+// host keeps W below kMaxCost, so that 32 bits hold every sum here.)
 constexpr long long kMaxCost = 1LL << 31;
-__host__ __device__ inline unsigned split_share(unsigned W, unsigned least) {
-  const unsigned even = (W + kSplitGrid - 1) / kSplitGrid;
-  return even > least ? even : least;
-}
-// Start of CTA c's stretch.
-__host__ __device__ inline unsigned split_start(unsigned W, unsigned c, unsigned share) {
-  return c * share < W ? c * share : W;
+__host__ __device__ inline unsigned split_start(unsigned W, unsigned c, unsigned least) {
+  const unsigned even = W / kSplitGrid, rest = W - even * kSplitGrid;
+  const unsigned x = even >= least ? c * even + (c < rest ? c : rest) : c * least;
+  return x < W ? x : W;
 }
 // The tile at which a boundary `r` units into an item cuts it (0: before the item).
 __host__ __device__ inline int split_tile(unsigned r) {
@@ -209,9 +206,8 @@ struct Scheduler {
       per_head += __reduce_add_sync(0xffffffffu, own);
     }
     const unsigned W = per_head * c.heads;
-    const unsigned share = split_share(W, least);
-    x0 = split_start(W, blockIdx.x, share);
-    x1 = split_start(W, blockIdx.x + 1, share);
+    x0 = split_start(W, blockIdx.x, least);
+    x1 = split_start(W, blockIdx.x + 1, least);
     at = x0;
     b = c.batch;
     h = p = 0;
