@@ -14,26 +14,31 @@
 //
 // Warp roles (384 threads; at launch every thread may hold 168 registers, then warpgroup 2
 // hands registers to warpgroups 0 and 1):
-//   warps 0-3, 4-7  softmax of query tile 0 and 1: thread r owns row r (TMEM lane r) and
-//                   the tile's 128 scores of it, so its maximum needs no exchange.
+//   warps 0-3, 4-7  softmax of query tile 0 and 1: thread r owns row r (TMEM lane r), so its
+//                   maximum needs no exchange. It takes a tile's keys in two halves of 64.
 //   warp 8          K producer: the item's two Q tiles, then K tiles into 2 stages.
 //   warp 10         V producer, 2 stages. Both walk the page table by themselves, a window
 //                   of pages ahead, one box per page and 64 columns.
 //   warp 11         scheduler: the CTA's items.
-//   warp 9          MMA issuer, in the order S0_j S1_j | PV0_j S0_j+1 PV1_j S1_j+1 | ...,
-//                   so that one warpgroup exponentiates while the tensor core multiplies
-//                   for the other. The order runs on across items: the next item's first
-//                   scores are computed while this one's outputs are stored.
+//   warp 9          MMA issuer. With S_g,h the scores of query tile g and half h of the tile
+//                   and PV_g,h their weights' product, it issues for each tile
+//                     PV_0,0 S_0,0  PV_1,0 S_1,0  PV_0,1 S_0,1  PV_1,1 S_1,1
+//                   each PV that of the tile before. The order runs on across items: the
+//                   next item's first scores are computed while this one's outputs leave.
+//
+// TMEM (512 columns at d = 128): 64 columns of scores per (g, h) at 128 g + 64 h, whose first
+// 32 the weights P take over; O of g at 256 + d g. Because a half's scores wait only for
+// the product of the half two before, they are there when the softmax has finished the half
+// in between: it never waits for the tensor core's round trip, which with whole-tile
+// buffers was half of its time. Products of a g run in order; O_g may be rescaled once the
+// product before has landed (a barrier, waited for only when a row's reference moves past
+// 2^8, and at the item's end).
 //
 // An item with one query tile (a single token among chunks, a short draft, a chunk's last
 // tokens) would leave one warpgroup idle and the tensor core waiting for the other. There
-// the two take the key tiles in turn, both with query tile 0 (order S0_j S1_j+1 PV0_j
-// S0_j+2 PV1_j+1 ...), and warpgroup 0 joins the two partial outputs out of tensor memory
-// by their log-sum-exps. Warps none of whose rows is a real query skip the softmax.
-//
-// TMEM (512 columns at d = 128): S and P of warpgroup g at 128 g, O of g at 256 + d g. MMAs
-// of one thread run in order, so S_g,j+1 complete implies P_g,j V_j complete and O_g may be
-// rescaled without a further wait; the reference of a row moves only past 2^8.
+// the two take the key tiles in turn, both with query tile 0, and warpgroup 0 joins the two
+// partial outputs out of tensor memory by their log-sum-exps. Warps none of whose rows is a
+// real query skip the softmax.
 //
 // Scores are in base 2. Two row sums: of the 16-bit weights that the product multiplies
 // (normalises O) and of the unrounded ones (gives L). V rows of keys that no row of the
@@ -70,8 +75,8 @@ struct ChunkLayout {
   static constexpr uint32_t kBar = kJoin + 128 * 8;
   static constexpr int bQFull = 0, bQEmpty = 1, bKFull = 2, bKEmpty = bKFull + kChunkKStages,
                        bVFull = bKEmpty + kChunkKStages, bVEmpty = bVFull + kChunkVStages,
-                       bSFull = bVEmpty + kChunkVStages, bPFull = bSFull + 2,
-                       bPHalf = bPFull + 2, bODone = bPHalf + 2, bJoin = bODone + 2,
+                       bSFull = bVEmpty + kChunkVStages,  // + 2 g + h, as the next two
+                       bPFull = bSFull + 4, bDone = bPFull + 4, bJoin = bDone + 4,
                        bJoined = bJoin + 1, bItems = bJoined + 1,
                        kNumBars = bItems + 2 * kItemSlots;
   static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
@@ -79,7 +84,7 @@ struct ChunkLayout {
   static constexpr uint32_t kBytes = kAbort + 8 + 1024;
   // at least 120 KB, so that one CTA and its 512 TMEM columns sit on each SM
   static constexpr uint32_t kSmem = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
-  static constexpr uint32_t tS = 0;    // + 128 * warpgroup
+  static constexpr uint32_t tS = 0;    // + 128 * warpgroup + 64 * half
   static constexpr uint32_t tO = 256;  // + D * warpgroup
 };
 
@@ -125,19 +130,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                           int least,
                           float scale_log2) {
   using Lay = ChunkLayout<D>;
-  // Of every 16 exponential pairs, two go to the FMA pipe at d = 128, none at d = 64, and
-  // at d = 64 P V is issued in two halves: measured on the contiguous forward, whose inner
-  // loop this is. (Masked scores may take the polynomial: its 2^-125 for them vanishes next
-  // to the row's own weights, and in a row without any nothing is read.)
+  // Of every 16 exponential pairs, kPolyPairs go to the FMA pipe. (Masked scores may take the
+  // polynomial: its 2^-125 for them vanishes next to the row's own weights, and in a row
+  // without any nothing is read.)
   constexpr int kPolyPairs = D == 64 ? 0 : 2;
   constexpr int kPolyStride = kPolyPairs > 0 ? 16 / kPolyPairs : 16;
-  constexpr bool kSplitPV = D == 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t pad = ((raw_base + 1023u) & ~1023u) - raw_base;
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = raw_base + pad;
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
   const int tpt = kKeyTile / group;  // tokens of a query tile
   // x / group for x < 128: ceil(2^16 / group) errs by less than 128 / 2^16 of a unit
@@ -158,11 +161,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(bar(Lay::bVFull + s), 1);
       mbar_init(bar(Lay::bVEmpty + s), 1);
     }
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(bar(Lay::bSFull + g), 1);
-      mbar_init(bar(Lay::bPFull + g), 128);
-      mbar_init(bar(Lay::bPHalf + g), 128);
-      mbar_init(bar(Lay::bODone + g), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(Lay::bSFull + i), 1);
+      mbar_init(bar(Lay::bPFull + i), 128);
+      mbar_init(bar(Lay::bDone + i), 1);
     }
     mbar_init(bar(Lay::bJoin), 128);
     mbar_init(bar(Lay::bJoined), 128);
@@ -255,84 +257,78 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (win.bad) atomicExch(&g_fa_status, kStatusInvalid);
   } else if (warp == kChunkMmaWarp) {
     // -------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16_f32(kKeyTile, kKeyTile, BF16, false, false);
+    {
+      constexpr uint32_t idesc_s = idesc_f16_f32(kKeyTile, 64, BF16, false, false);
       constexpr uint32_t idesc_o = idesc_f16_f32(kKeyTile, D, BF16, false, true);
-      // A tile's turns: the product that query tile 0 owes, 0's scores of this tile, the same
-      // for 1. Where both owe one and both see the tile -- all but an item's edges -- they
-      // are laid out straight; otherwise one body with a run-time g serves every case, since
-      // copies for each made this warp's code 16 KB, which the softmax warps' and it kept
-      // pushing out of the instruction cache, at three times the cost for all code that
-      // runs once an item. (The run-time body alone costs the straight path 12 %.)
+      // Where every (g, h) owes a product and sees the tile -- all but an item's edges -- the
+      // turns are laid out straight: this one thread feeds the tensor core, and with run-time
+      // g and h its own instructions take twice the time of what it issues. All other cases
+      // share one body with run-time g and h: copies for each made this warp's code 16 KB,
+      // and it and the softmax warps' kept pushing each other out of the instruction cache,
+      // at three times the cost for all code that runs once an item.
       int ks = 0, item = 0;
-      uint32_t kphase = 0, pphase0 = 0, pphase1 = 0;
-      // what g owes: 0 nothing, else 1 (an item's first product: O is overwritten) or 2, + 4
-      // for the item's last, + 8 times the V tile's index among the CTA's
-      uint32_t owed0 = 0, owed1 = 0;
+      uint32_t kphase = 0, pphase = 0;  // pphase: bit 2 g + h
+      // what (g, h) owes: 0 nothing, else 1 (an item's first product: O is overwritten) or 2,
+      // + 4 times the V tile's index among the CTA's
+      uint32_t owed[4] = {0, 0, 0, 0};
       uint32_t vi = 0;  // V tiles before this one
       bool more = true;
       while (ok && more) {
-        more = ring.get(&w, &ok, abort_flag);
+        more = __all_sync(0xffffffffu, ring.get(&w, &ok, abort_flag));
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (more) {
-          ring.read(true);
+          ring.read(lane == 0);
           if (w.j0 >= w.j1) continue;
         }
-        const ChunkTiles t(w, tpt, wl, wr);
+        ChunkTiles t(w, tpt, wl, wr);
+        t.one = __all_sync(0xffffffffu, t.one);
+        t.first = __shfl_sync(0xffffffffu, t.first, 0);
+        t.last = __shfl_sync(0xffffffffu, t.last, 0);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          t.lo[g] = __shfl_sync(0xffffffffu, t.lo[g], 0);
+          t.hi[g] = __shfl_sync(0xffffffffu, t.hi[g], 0);
+        }
         // after the last item, one turn for the products that are owed
         const int last = more ? t.last : t.first + 1;
         for (int tile = t.first; ok && tile < last; ++tile) {
-          if (more && !t.one && owed0 != 0 && owed1 != 0 && t.in(0, tile) && t.in(1, tile) &&
-              tile > t.first) {
-            const uint32_t v = owed0 >> 3;
+          if (more && !t.one && tile > t.first && owed[0] && owed[1] && owed[2] && owed[3] &&
+              t.in(0, tile) && t.in(1, tile)) {
+            const uint32_t v = vi - 1;  // owed by all four
             const uint32_t vs = v % kChunkVStages;
-            const uint64_t dv =
-                sdesc_sw128(sbase + Lay::kV + vs * Lay::kTileBytes, Lay::kChunkBytes, 1024);
-            const uint64_t dk = sdesc_sw128(sbase + Lay::kK + ks * Lay::kTileBytes, 16, 1024);
+            const SmemDesc dv =
+                smem_desc(sbase + Lay::kV + vs * Lay::kTileBytes, Lay::kChunkBytes, 1024);
+            const SmemDesc dk = smem_desc(sbase + Lay::kK + ks * Lay::kTileBytes, 16, 1024);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const uint32_t what = g ? owed1 : owed0;
-              const uint32_t parity = g ? pphase1 : pphase0;
-              const uint32_t d_s = tmem + Lay::tS + g * 128, d_o = tmem + Lay::tO + g * D;
-              ok = mbar_wait(bar((kSplitPV ? Lay::bPHalf : Lay::bPFull) + g), parity,
-                             abort_flag) &&
-                   (g == 1 || mbar_wait(bar(Lay::bVFull + vs), (v / kChunkVStages) & 1,
-                                        abort_flag));
+            for (int turn = 0; turn < 4; ++turn) {
+              const int h = turn >> 1, g = turn & 1, i = 2 * g + h;
+              const uint32_t d_s = tmem + Lay::tS + g * 128 + h * 64, d_o = tmem + Lay::tO + g * D;
+              ok = warp_wait(bar(Lay::bPFull + i), pphase >> i & 1u, abort_flag) &&
+                   (turn > 0 || (warp_wait(bar(Lay::bVFull + vs), (v / kChunkVStages) & 1,
+                                           abort_flag) &&
+                                 warp_wait(bar(Lay::bKFull + ks), kphase, abort_flag)));
               if (!ok) break;
               tc_fence_after();
-              const uint32_t accumulate = (what & 3u) == 2u ? 1u : 0u;
 #pragma unroll
-              for (int k = 0; k < kKeyTile / 32; ++k)
-                mma_ts(d_o, d_s + k * 8, sdesc_step(dv, k * 2048), idesc_o,
-                       k > 0 ? 1u : accumulate);
-              if (kSplitPV) {
-                ok = mbar_wait(bar(Lay::bPFull + g), parity, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-              }
-#pragma unroll
-              for (int k = kKeyTile / 32; k < kKeyTile / 16; ++k)
-                mma_ts(d_o, d_s + k * 8, sdesc_step(dv, k * 2048), idesc_o, 1u);
-              if (g == 0) {
-                ok = mbar_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              const uint64_t dq = sdesc_sw128(sbase + Lay::kQ + g * Lay::kTileBytes, 16, 1024);
+              for (int k = 0; k < 4; ++k)
+                warp_mma_ts(d_o, d_s + k * 8, dv, h * 8192 + k * 2048, idesc_o,
+                       k > 0 ? 1u : (owed[i] & 3u) - 1u);
+              warp_mma_commit(bar(Lay::bDone + i));
+              const SmemDesc dq = smem_desc(sbase + Lay::kQ + g * Lay::kTileBytes, 16, 1024);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
                 const uint32_t koff = (k >> 2) * Lay::kChunkBytes + (k & 3) * 32;
-                mma_ss(d_s, sdesc_step(dq, koff), sdesc_step(dk, koff), idesc_s, k > 0 ? 1u : 0u);
+                warp_mma_ss(d_s, dq, koff, dk, h * 8192 + koff, idesc_s,
+                       k > 0 ? 1u : 0u);
               }
-              mma_commit(bar(Lay::bSFull + g));
+              warp_mma_commit(bar(Lay::bSFull + i));
+              owed[i] = 2u + 4u * vi;
             }
             if (!ok) break;
-            mma_commit(bar(Lay::bVEmpty + vs));
-            mma_commit(bar(Lay::bKEmpty + ks));
-            pphase0 ^= 1;
-            pphase1 ^= 1;
-            owed0 = 2u + (t.last_of(0, tile) ? 4u : 0u) + 8u * vi;
-            owed1 = 2u + (t.last_of(1, tile) ? 4u : 0u) + 8u * vi;
+            warp_mma_commit(bar(Lay::bVEmpty + vs));
+            warp_mma_commit(bar(Lay::bKEmpty + ks));
+            pphase ^= 15u;
             ++vi;
             if (++ks == kChunkKStages) {
               ks = 0;
@@ -342,74 +338,61 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           // an item's first tile: both groups (the item before may have left products owed)
           const bool alone = t.one && tile > t.first;
-          int g = alone ? (tile - t.first) & 1 : 0;
           bool k_waited = false;
 #pragma unroll 1
-          for (int turns = alone ? 1 : 2; turns > 0; --turns, g ^= 1) {
-            const uint32_t what = g ? owed1 : owed0;
-            const uint32_t d_s = tmem + Lay::tS + g * 128;  // S, and P packed in 64 columns
+          for (int turn = 0; turn < 4; ++turn) {
+            const int h = turn >> 1, g = turn & 1, i = 2 * g + h;
+            if (alone && g != ((tile - t.first) & 1)) continue;
+            const uint32_t what = g ? (h ? owed[3] : owed[2]) : (h ? owed[1] : owed[0]);
+            const uint32_t d_s = tmem + Lay::tS + g * 128 + h * 64;
+            uint32_t next = 0;
             if (what != 0) {
-              const uint32_t parity = g ? pphase1 : pphase0;
-              const uint32_t v = what >> 3;
+              const uint32_t v = what >> 2;
               const uint32_t vs = v % kChunkVStages;
-              ok = mbar_wait(bar((kSplitPV ? Lay::bPHalf : Lay::bPFull) + g), parity,
-                             abort_flag) &&
-                   mbar_wait(bar(Lay::bVFull + vs), (v / kChunkVStages) & 1, abort_flag);
+              ok = warp_wait(bar(Lay::bPFull + i), pphase >> i & 1u, abort_flag) &&
+                   warp_wait(bar(Lay::bVFull + vs), (v / kChunkVStages) & 1, abort_flag);
               if (!ok) break;
               tc_fence_after();
-              const uint64_t dv =
-                  sdesc_sw128(sbase + Lay::kV + vs * Lay::kTileBytes, Lay::kChunkBytes, 1024);
+              const SmemDesc dv = smem_desc(sbase + Lay::kV + vs * Lay::kTileBytes + h * 8192,
+                                              Lay::kChunkBytes, 1024);
               const uint32_t d_o = tmem + Lay::tO + g * D;
-              const uint32_t accumulate = (what & 3u) == 2u ? 1u : 0u;
 #pragma unroll
-              for (int k = 0; k < kKeyTile / 32; ++k)
-                mma_ts(d_o, d_s + k * 8, sdesc_step(dv, k * 2048), idesc_o,
-                       k > 0 ? 1u : accumulate);
-              if (kSplitPV) {
-                ok = mbar_wait(bar(Lay::bPFull + g), parity, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-              }
+              for (int k = 0; k < 4; ++k)
+                warp_mma_ts(d_o, d_s + k * 8, dv, k * 2048, idesc_o,
+                       k > 0 ? 1u : (what & 3u) - 1u);
+              warp_mma_commit(bar(Lay::bDone + i));
+              pphase ^= 1u << i;
+              // the V tile is released with the last product that is owed for it
+              bool others = false;
 #pragma unroll
-              for (int k = kKeyTile / 32; k < kKeyTile / 16; ++k)
-                mma_ts(d_o, d_s + k * 8, sdesc_step(dv, k * 2048), idesc_o, 1u);
-              if (what & 4u) mma_commit(bar(Lay::bODone + g));
-              const uint32_t other = g ? owed0 : owed1;
-              if (other == 0 || other >> 3 != v) mma_commit(bar(Lay::bVEmpty + vs));
-              if (g) {
-                pphase1 ^= 1;
-                owed1 = 0;
-              } else {
-                pphase0 ^= 1;
-                owed0 = 0;
-              }
+              for (int k = 0; k < 4; ++k)
+                others = others || (k != i && owed[k] != 0 && owed[k] >> 2 == v);
+              if (!others) warp_mma_commit(bar(Lay::bVEmpty + vs));
             }
             if (more && t.in(g, tile)) {
               if (tile == t.first)
-                ok = mbar_wait(bar(Lay::bQFull), static_cast<uint32_t>(item) & 1, abort_flag);
-              if (ok && !k_waited) ok = mbar_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
+                ok = warp_wait(bar(Lay::bQFull), static_cast<uint32_t>(item) & 1, abort_flag);
+              if (ok && !k_waited) ok = warp_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
               if (!ok) break;
               k_waited = true;
               tc_fence_after();
-              const uint64_t dq =
-                  sdesc_sw128(sbase + Lay::kQ + (t.one ? 0 : g) * Lay::kTileBytes, 16, 1024);
-              const uint64_t dk = sdesc_sw128(sbase + Lay::kK + ks * Lay::kTileBytes, 16, 1024);
+              const SmemDesc dq =
+                  smem_desc(sbase + Lay::kQ + (t.one ? 0 : g) * Lay::kTileBytes, 16, 1024);
+              const SmemDesc dk =
+                  smem_desc(sbase + Lay::kK + ks * Lay::kTileBytes + h * 8192, 16, 1024);
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
                 const uint32_t koff = (k >> 2) * Lay::kChunkBytes + (k & 3) * 32;
-                mma_ss(d_s, sdesc_step(dq, koff), sdesc_step(dk, koff), idesc_s, k > 0 ? 1u : 0u);
+                warp_mma_ss(d_s, dq, koff, dk, koff, idesc_s, k > 0 ? 1u : 0u);
               }
-              mma_commit(bar(Lay::bSFull + g));
-              const uint32_t next = (tile == (g ? t.lo[1] : t.lo[0]) ? 1u : 2u) +
-                                    (t.last_of(g, tile) ? 4u : 0u) + 8u * vi;
-              if (g)
-                owed1 = next;
-              else
-                owed0 = next;
+              warp_mma_commit(bar(Lay::bSFull + i));
+              next = (h == 0 && tile == (g ? t.lo[1] : t.lo[0]) ? 1u : 2u) + 4u * vi;
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) owed[k] = k == i ? next : owed[k];
           }
           if (!ok || !more) break;
-          mma_commit(bar(Lay::bKEmpty + ks));
+          warp_mma_commit(bar(Lay::bKEmpty + ks));
           ++vi;
           if (++ks == kChunkKStages) {
             ks = 0;
@@ -417,7 +400,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         if (!ok || !more) break;
-        mma_commit(bar(Lay::bQEmpty));
+        warp_mma_commit(bar(Lay::bQEmpty));
         ++item;
       }
     }
@@ -430,10 +413,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int tr = r * by_group >> 16;  // its token in the tile (tpt or more: a row of zeros)
     const int head_in = r - tr * group;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t s_cols = Lay::tS + g * 128;
     const uint32_t o_cols = Lay::tO + g * D;
     const uint64_t c2 = f2_pack(scale_log2, scale_log2);
-    uint32_t sphase = 0, ophase = 0, jphase = 0;
+    uint32_t used = 0;  // tiles of this group before: phases of its S, P and product barriers
+    uint32_t jphase = 0;
     int vi = 0;  // V tiles of the CTA before this item
     while (ok) {
       if (!__all_sync(0xffffffffu, ring.get(&w, &ok, abort_flag))) break;
@@ -460,150 +443,150 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       float m = -INFINITY;  // running reference, base-2 scaled units
       float l = 0.f;        // row sum of p
       float l_o = 0.f;      // row sum of the 16-bit-rounded p
-      for (int tile = lo; ok && tile < hi; tile += step) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bSFull + g), sphase, abort_flag));
-        if (!ok) break;
-        sphase ^= 1;
-        tc_fence_after();
-        const int key0 = tile * kKeyTile;
-        const bool edge = key0 < all_lo || key0 + kKeyTile - 1 > all_hi;
-        if (edge && (key0 < w.keys.lo || key0 + kKeyTile - 1 > w.keys.hi)) {
-          // keys that no row of the item sees: their V rows become zeros (by all warps)
-          const int v = vi + tile - first;
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(bar(Lay::bVFull + v % kChunkVStages),
-                                    static_cast<uint32_t>(v / kChunkVStages) & 1, abort_flag));
-          if (!ok) break;
-          if (key0 + r < w.keys.lo || key0 + r > w.keys.hi) {
-            const uint32_t row = sbase + Lay::kV + (v % kChunkVStages) * Lay::kTileBytes + r * 128;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                               row + (i >> 3) * Lay::kChunkBytes + (i & 7) * 16),
-                           "r"(0)
-                           : "memory");
-          }
-          fence_async_smem();
-        }
-        if (!busy) {
-          tc_fence_before();
-          if (kSplitPV) mbar_arrive(bar(Lay::bPHalf + g));
-          mbar_arrive(bar(Lay::bPFull + g));
-          continue;
-        }
-        // An edge of the mask: columns [first_col, last_col] of the row are visible, the
-        // others become -inf in tensor memory. 32 columns at a time in a loop, off the main
-        // path: unrolled on the registers below it tripled an edge tile's time, most of it
-        // spent fetching instructions that few tiles run.
-        if (edge) {
-          const int first_col = row_lo - key0, last_col = row_hi - key0;
+      for (int tile = lo; ok && tile < hi; tile += step, ++used) {
 #pragma unroll 1
-          for (int h = 0; h < 4; ++h) {
-            const int lo_bit = first_col - 32 * h, hi_bit = last_col - 32 * h;
-            uint32_t seen = hi_bit < 0 ? 0u : 0xffffffffu >> (31 - min(hi_bit, 31));
-            seen &= lo_bit > 31 ? 0u : 0xffffffffu << max(lo_bit, 0);
-            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
-            uint32_t x[32];
-            if (__any_sync(0xffffffffu, seen != 0)) {
-              tmem_ld32(lane_base + s_cols + h * 32, x);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t bars = 2 * g + h;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bSFull + bars), used & 1, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t s_cols = Lay::tS + g * 128 + h * 64;
+          const int key0 = tile * kKeyTile + h * 64;
+          const bool edge = key0 < all_lo || key0 + 63 > all_hi;
+          if (edge && (key0 < w.keys.lo || key0 + 63 > w.keys.hi)) {
+            // keys that no row of the item sees: their V rows become zeros (by all warps)
+            const int v = vi + tile - first;
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(bar(Lay::bVFull + v % kChunkVStages),
+                                      static_cast<uint32_t>(v / kChunkVStages) & 1, abort_flag));
+            if (!ok) break;
+            const int key = key0 + (r & 63);
+            if (key < w.keys.lo || key > w.keys.hi) {  // rows r and r + 64: half the columns each
+              const uint32_t row = sbase + Lay::kV + (v % kChunkVStages) * Lay::kTileBytes +
+                                   (key - tile * kKeyTile) * 128;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const int at = i + (r >> 6) * (D / 16);  // 16-byte piece of the row
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 row + (at >> 3) * Lay::kChunkBytes + (at & 7) * 16),
+                             "r"(0)
+                             : "memory");
+              }
+            }
+            fence_async_smem();
+          }
+          if (!busy) {
+            tc_fence_before();
+            mbar_arrive(bar(Lay::bPFull + bars));
+            continue;
+          }
+          // An edge of the mask: columns [first_col, last_col] of the row are visible, the
+          // others become -inf in tensor memory. 32 columns at a time in a loop, off the main
+          // path: unrolled on the registers below it tripled an edge tile's time, most of it
+          // spent fetching instructions that few tiles run.
+          if (edge) {
+            const int first_col = row_lo - key0, last_col = row_hi - key0;
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              const int lo_bit = first_col - 32 * i, hi_bit = last_col - 32 * i;
+              uint32_t seen = hi_bit < 0 ? 0u : 0xffffffffu >> (31 - min(hi_bit, 31));
+              seen &= lo_bit > 31 ? 0u : 0xffffffffu << max(lo_bit, 0);
+              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+              uint32_t x[32];
+              tmem_ld32(lane_base + s_cols + i * 32, x);
               tmem_wait_ld();
               reg_fence32(x);
-            } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = 0u;
+              for (int k = 0; k < 32; ++k) x[k] = seen >> k & 1 ? x[k] : 0xff800000u;
+              tmem_st32(lane_base + s_cols + i * 32, x);
             }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1 ? x[i] : 0xff800000u;
-            tmem_st32(lane_base + s_cols + h * 32, x);
+            tmem_wait_st();
           }
-          tmem_wait_st();
-        }
-        float s[128];
-        {
-          uint32_t sr[128];
+          float s[64];
+          {
+            uint32_t sr[64];
+            tmem_ld32(lane_base + s_cols, sr);
+            tmem_ld32(lane_base + s_cols + 32, sr + 32);
+            tmem_wait_ld();
+            reg_fence32(sr);
+            reg_fence32(sr + 32);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(lane_base + s_cols + i * 32, sr + i * 32);
-          tmem_wait_ld();
+            for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(sr[e]);
+          }
+          // row maximum over four independent chains
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) reg_fence32(sr + i * 32);
+          for (int i = 0; i < 64; i += 8) {
 #pragma unroll
-          for (int e = 0; e < 128; ++e) s[e] = __uint_as_float(sr[e]);
-        }
-        // row maximum over four independent chains
-        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int k = 0; k < 4; ++k) mq[k] = fmax3(mq[k], s[i + 2 * k], s[i + 2 * k + 1]);
+          }
+          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+          const float cand = mx * scale_log2;
+          const float m_new = (cand > m + kChunkRescaleSlack) ? cand : m;
+          // a row that has seen no key keeps m = -inf: alpha = 1, and 0 is subtracted
+          const bool empty_row = m_new == -INFINITY;
+          const float alpha = empty_row ? 1.f : ex2_approx(m - m_new);  // 0 at first
+          const float m_sub = empty_row ? 0.f : m_new;
+          const uint64_t nm2 = f2_pack(-m_sub, -m_sub);
+          uint64_t sum2[2] = {0, 0}, sum2_o[2] = {0, 0};  // packed +0.0f
 #pragma unroll
-        for (int i = 0; i < 128; i += 8) {
+          for (int j = 0; j < 2; ++j) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mq[k] = fmax3(mq[k], s[i + 2 * k], s[i + 2 * k + 1]);
-        }
-        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-        const float cand = mx * scale_log2;
-        const float m_new = (cand > m + kChunkRescaleSlack) ? cand : m;
-        // a row that has seen no key keeps m = -inf: alpha = 1, and 0 is subtracted
-        const bool empty_row = m_new == -INFINITY;
-        const float alpha = empty_row ? 1.f : ex2_approx(m - m_new);  // 0 at first
-        const float m_sub = empty_row ? 0.f : m_new;
-        const uint64_t nm2 = f2_pack(-m_sub, -m_sub);
-        auto rescale_o = [&]() {
-          if (tile > lo && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
+              const int e = j * 32 + 2 * i;
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, nm2), x0, x1);
+              float p0, p1;
+              if (kPolyPairs > 0 && i % kPolyStride == kPolyStride - 1) {
+                ex2_poly_pair(x0, x1, p0, p1);
+              } else {
+                p0 = ex2_approx(x0);
+                p1 = ex2_approx(x1);
+              }
+              pk[i] = pack2<BF16>(p0, p1);
+              float r0, r1;
+              unpack2<BF16>(pk[i], r0, r1);
+              sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
+              sum2_o[i & 1] = f2_add(sum2_o[i & 1], f2_pack(r0, r1));
+            }
+            tmem_st16(lane_base + s_cols + j * 16, pk);
+          }
+          float a0, a1, b0, b1;
+          f2_unpack(f2_add(sum2[0], sum2[1]), a0, a1);
+          f2_unpack(f2_add(sum2_o[0], sum2_o[1]), b0, b1);
+          l = l * alpha + (a0 + a1);
+          l_o = l_o * alpha + (b0 + b1);
+          // a reference moved, and O holds products: once the last of them has landed (that
+          // of the half before; the one before that landed ahead of these scores)
+          if ((tile > lo || h > 0) && __any_sync(0xffffffffu, alpha != 1.f)) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bDone + (bars ^ 1)),
+                                                   (h ? used : used - 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
               uint32_t o[32];
-              tmem_ld32(lane_base + o_cols + i * 32, o);
+              tmem_ld32(lane_base + o_cols + i, o);
               tmem_wait_ld();
               reg_fence32(o);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st32(lane_base + o_cols + i * 32, o);
+              tmem_st32(lane_base + o_cols + i, o);
             }
           }
-        };
-        if (kSplitPV) rescale_o();
-        uint64_t sum2[2] = {0, 0}, sum2_o[2] = {0, 0};  // packed +0.0f
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int e = h * 32 + 2 * i;
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, nm2), x0, x1);
-            float p0, p1;
-            if (kPolyPairs > 0 && i % kPolyStride == kPolyStride - 1) {
-              ex2_poly_pair(x0, x1, p0, p1);
-            } else {
-              p0 = ex2_approx(x0);
-              p1 = ex2_approx(x1);
-            }
-            pk[i] = pack2<BF16>(p0, p1);
-            float r0, r1;
-            unpack2<BF16>(pk[i], r0, r1);
-            sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
-            sum2_o[i & 1] = f2_add(sum2_o[i & 1], f2_pack(r0, r1));
-          }
-          tmem_st16(lane_base + s_cols + h * 16, pk);
-          if (kSplitPV && h == 1) {  // keys 0-63 (and a rescaled O) are in TMEM
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(bar(Lay::bPHalf + g));
-          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(Lay::bPFull + bars));
+          m = m_new;
         }
-        float a0, a1, b0, b1;
-        f2_unpack(f2_add(sum2[0], sum2[1]), a0, a1);
-        f2_unpack(f2_add(sum2_o[0], sum2_o[1]), b0, b1);
-        l = l * alpha + (a0 + a1);
-        l_o = l_o * alpha + (b0 + b1);
-        if (!kSplitPV) rescale_o();
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(Lay::bPFull + g));
-        m = m_new;
       }
       vi += w.j1 - w.j0;
       const bool some = lo < hi;
-      ok = __all_sync(0xffffffffu, ok && (!some || mbar_wait(bar(Lay::bODone + g), ophase,
-                                                            abort_flag)));
-      ophase ^= some;
+      ok = __all_sync(
+          0xffffffffu,
+          ok && (!some || (mbar_wait(bar(Lay::bDone + 2 * g), (used - 1) & 1, abort_flag) &&
+                           mbar_wait(bar(Lay::bDone + 2 * g + 1), (used - 1) & 1, abort_flag))));
       tc_fence_after();
       // rows that see no key: O = 0, L = -inf (their sums need not be 0: the polynomial's
       // least value is 2^-125)

@@ -79,6 +79,55 @@ __device__ __forceinline__ float reduce_columns(float* v, int lane, Op op) {
   if (C == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
   return v[0];
 }
+// MMAs issued by a whole converged warp, one lane of it elected. A shared-memory descriptor
+// is two words of which only the low one (address and leading offset) moves: kept apart
+// and the same in all lanes, they can live in uniform registers, where the instruction
+// wants them; from a branch of lane 0 every descriptor of every MMA is moved there first.
+struct SmemDesc {
+  uint32_t lo, hi;
+};
+// 128-byte swizzle; byte offsets of the leading and the stride dimension.
+__device__ __forceinline__ SmemDesc smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return {(saddr >> 4 & 0x3FFFu) | (lbo >> 4) << 16, (sbo >> 4) | 1u << 14 | 2u << 29};
+}
+__device__ __forceinline__ void warp_mma_ss(uint32_t d, SmemDesc a, uint32_t a_bytes, SmemDesc b,
+                                            uint32_t b_bytes, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 da, {%1, %2};\n\t"
+      "mov.b64 db, {%3, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}\n" ::"r"(d),
+      "r"(a.lo + (a_bytes >> 4)), "r"(a.hi), "r"(b.lo + (b_bytes >> 4)), "r"(b.hi), "r"(idesc),
+      "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void warp_mma_ts(uint32_t d, uint32_t a, SmemDesc b, uint32_t b_bytes,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b.lo + (b_bytes >> 4)), "r"(b.hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void warp_mma_commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(
+          bar)
+      : "memory");
+}
+// A wait by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 // Four consecutive 32-bit TMEM columns of this warp's lanes.
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
