@@ -40,9 +40,13 @@
 // partial outputs out of tensor memory by their log-sum-exps. Warps none of whose rows is a
 // real query skip the softmax.
 //
-// Scores are in base 2. Two row sums: of the 16-bit weights that the product multiplies
-// (normalises O) and of the unrounded ones (gives L). V rows of keys that no row of the
-// item sees are zeroed in shared memory before they are multiplied by weights of 0.
+// Scores are in base 2. One row sum, of the unrounded weights, gives L and normalises O. (The
+// product multiplies weights rounded to 16 bits. A second sum, of those, would make O an
+// exact average with them, which only rows that a few keys dominate would notice -- their
+// weights' common rounding, at most half a step of O, would cancel -- and cost three of
+// the eight instructions per pair of scores in a loop that is bound by them.) V rows of keys
+// that no row of the item sees are zeroed in shared memory before they are multiplied by
+// weights of 0.
 #pragma once
 
 #include "fa_paged_step.cuh"
@@ -130,11 +134,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                           int least,
                           float scale_log2) {
   using Lay = ChunkLayout<D>;
-  // Of every 16 exponential pairs, kPolyPairs go to the FMA pipe. (Masked scores may take the
-  // polynomial: its 2^-125 for them vanishes next to the row's own weights, and in a row
-  // without any nothing is read.)
-  constexpr int kPolyPairs = D == 64 ? 0 : 2;
-  constexpr int kPolyStride = kPolyPairs > 0 ? 16 / kPolyPairs : 16;
+  // Of every 16 exponential pairs, kPolyPairs go to the FMA pipe: 2048 tokens over 16k keys
+  // (32 heads) take 447 / 444 / 431 / 428 us at d = 128 with 0 / 1 / 2 / 4 of them, 369 / 357 /
+  // 376 at d = 64 with 0 / 2 / 4. (Masked scores may take the polynomial: its 2^-125 for them
+  // vanishes next to the row's own weights, and in a row without any nothing is read.)
+  constexpr int kPolyPairs = D == 64 ? 2 : 4;
+  constexpr int kPolyStride = 16 / kPolyPairs;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t pad = ((raw_base + 1023u) & ~1023u) - raw_base;
@@ -442,7 +447,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int row_lo = mid - wl, row_hi = min(w.nk - 1, mid + wr);
       float m = -INFINITY;  // running reference, base-2 scaled units
       float l = 0.f;        // row sum of p
-      float l_o = 0.f;      // row sum of the 16-bit-rounded p
       for (int tile = lo; ok && tile < hi; tile += step, ++used) {
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const float alpha = empty_row ? 1.f : ex2_approx(m - m_new);  // 0 at first
           const float m_sub = empty_row ? 0.f : m_new;
           const uint64_t nm2 = f2_pack(-m_sub, -m_sub);
-          uint64_t sum2[2] = {0, 0}, sum2_o[2] = {0, 0};  // packed +0.0f
+          uint64_t sum2[2] = {0, 0};  // packed +0.0f
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             uint32_t pk[16];
@@ -538,25 +542,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               float x0, x1;
               f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, nm2), x0, x1);
               float p0, p1;
-              if (kPolyPairs > 0 && i % kPolyStride == kPolyStride - 1) {
+              if (i % kPolyStride == kPolyStride - 1) {
                 ex2_poly_pair(x0, x1, p0, p1);
               } else {
                 p0 = ex2_approx(x0);
                 p1 = ex2_approx(x1);
               }
               pk[i] = pack2<BF16>(p0, p1);
-              float r0, r1;
-              unpack2<BF16>(pk[i], r0, r1);
               sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
-              sum2_o[i & 1] = f2_add(sum2_o[i & 1], f2_pack(r0, r1));
             }
             tmem_st16(lane_base + s_cols + j * 16, pk);
           }
-          float a0, a1, b0, b1;
+          float a0, a1;
           f2_unpack(f2_add(sum2[0], sum2[1]), a0, a1);
-          f2_unpack(f2_add(sum2_o[0], sum2_o[1]), b0, b1);
           l = l * alpha + (a0 + a1);
-          l_o = l_o * alpha + (b0 + b1);
           // a reference moved, and O holds products: once the last of them has landed (that
           // of the half before; the one before that landed ahead of these scores)
           if ((tile > lo || h > 0) && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -592,7 +591,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // least value is 2^-125)
       const bool none = m == -INFINITY;
       float L2 = none ? -INFINITY : m + log2f(l);
-      float inv_l = none || l_o == 0.f ? 0.f : 1.f / l_o;
+      float inv_l = none ? 0.f : 1.f / l;
       float inv_other = 0.f;
       float2* join = reinterpret_cast<float2*>(smem + Lay::kJoin);
       if (one && ok) {  // group 1 hands over
@@ -613,7 +612,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
       }
-      // O / l_o: a thread holds a row, a store wants rows' neighbours side by side, so 128
+      // O / l: a thread holds a row, a store wants rows' neighbours side by side, so 128
       // bytes of each row (64 columns, or 32 of a part in fp32) at a time go through the
       // warp's 4 KB of shared memory, 128-byte-swizzled, and leave in one TMA store (of a
       // part's rows, or of whole tokens when 32 rows are that) or, at a sequence's ragged end,
