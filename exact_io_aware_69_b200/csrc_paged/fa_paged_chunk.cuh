@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                          static_cast<uint32_t>(pages.count * pages.rows) * D * 2);
         __syncwarp();
         load_tile_pages<D>(pages, tile, c.page_shift, win, map, tiles + st * Lay::kTileBytes,
-                           bar(full + st), nullptr, 0, 0, w.h, lane);
+                           bar(full + st), w.h, lane);
         if (++st == stages) {
           st = 0;
           phase ^= 1;

@@ -123,6 +123,17 @@ __device__ __forceinline__ void warp_mma_commit(uint32_t bar) {
           bar)
       : "memory");
 }
+// A 4-D tiled load by a whole converged warp (all arguments the same in every lane).
+__device__ __forceinline__ void warp_tma_load_4d(uint32_t dst, const CUtensorMap* map, int x,
+                                                 int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 // A wait by a whole warp: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
@@ -190,14 +201,16 @@ struct PageWindow {
     now = fetch(base + lane);
     then = fetch(base + 32 + lane);
   }
-  // Page i of the sequence, for every lane its own i (ascending over calls; all lanes' i
-  // lie in one window).
-  __device__ __forceinline__ int get(int i, int first, int lane) {
+  // Moves on until page `first` is in the window (calls ascend).
+  __device__ __forceinline__ void advance(int first, int lane) {
     while (first >= base + 32) {
       base += 32;
       now = then;
       then = fetch(base + 32 + lane);
     }
+  }
+  // Page i of the sequence, of the window; the same i in every lane.
+  __device__ __forceinline__ int get(int i) {
     int p = __shfl_sync(0xffffffffu, now, (i - base) & 31);
     if (static_cast<unsigned>(p) >= static_cast<unsigned>(pages)) {
       p = pages;

@@ -94,9 +94,8 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t* r) {
   }
 }
 
-// Issues the loads of the pages of tile `tile` that hold keys of [keys.lo, keys.hi] into
-// `vdst` and `kdst`, by all lanes of a warp: up to 8 pages x (K, V) x 64-column chunks.
-// Returns the pages' count times a page's rows, known before any load is issued.
+// The pages of tile `tile` that hold keys of [keys.lo, keys.hi]: up to 8, of which a box of
+// `rows` rows and 64 columns each is loaded.
 struct TilePages {
   int first, count;  // pages of the sequence
   int rows;          // of a page in this tile
@@ -107,25 +106,22 @@ struct TilePages {
     rows = min(1 << shift, kKeyTile);
   }
 };
+// Issued box by box by the converged warp: with a box per lane each took ~85 cycles (its
+// operands go to uniform registers one lane at a time), a tile of 16-row pages 1400.
 template <int D>
 __device__ __forceinline__ void load_tile_pages(const TilePages& t, int tile, int shift,
-                                                PageWindow& win, const CUtensorMap* mapA,
-                                                uint32_t dstA, uint32_t barA,
-                                                const CUtensorMap* mapB, uint32_t dstB,
-                                                uint32_t barB, int head, int lane) {
-  constexpr int kChunks = D / 64;
-  const int per_page = (mapB != nullptr ? 2 : 1) * kChunks;
-  // lane -> (page, operand, chunk); 8 pages x 4 pieces at most, one per lane
-  const int i = lane / per_page;
-  const int piece = lane - i * per_page;
-  const int page = win.get(t.first + min(i, t.count - 1), t.first, lane);
-  if (i < t.count) {
+                                                PageWindow& win, const CUtensorMap* map,
+                                                uint32_t dst, uint32_t bar, int head, int lane) {
+  win.advance(t.first, lane);
+#pragma unroll 1
+  for (int i = 0; i < t.count; ++i) {
+    const int page = win.get(t.first + i);
     const int key = max((t.first + i) << shift, tile * kKeyTile);  // first key of the box
-    const bool second = piece >= kChunks;
-    const int chunk = second ? piece - kChunks : piece;
-    const uint32_t at = static_cast<uint32_t>(chunk * kKeyTile + key - tile * kKeyTile) * 128u;
-    tma_load_4d((second ? dstB : dstA) + at, second ? mapB : mapA, chunk * 64,
-                key & ((1 << shift) - 1), head, page, second ? barB : barA);
+    const uint32_t at = dst + static_cast<uint32_t>(key - tile * kKeyTile) * 128u;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      warp_tma_load_4d(at + c * kKeyTile * 128, map, c * 64, key & ((1 << shift) - 1), head, page,
+                       bar);
   }
 }
 
@@ -146,7 +142,7 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
   const uint32_t pad = ((raw_base + 1023u) & ~1023u) - raw_base;
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = raw_base + pad;
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sbase + Lay::kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::kAbort);
@@ -242,57 +238,55 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
                          static_cast<uint32_t>(pages.count * pages.rows) * D * 2);
         __syncwarp();
         load_tile_pages<D>(pages, tile, c.page_shift, win, map, at + st * Lay::kStageBytes,
-                           bar(Lay::bFull + st), nullptr, 0, 0, w.h, lane);
+                           bar(Lay::bFull + st), w.h, lane);
       }
     }
     if (win.bad) atomicExch(&g_fa_status, kStatusInvalid);
   } else if (warp == kMma) {
     // -------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    {
       constexpr uint32_t id_s = idesc_f16_f32(kKeyTile, NQ, BF16, false, false);
       constexpr uint32_t id_o = idesc_f16_f32(128, NQ, BF16, true, false);
       // O^T += V^T P^T of tile t of the CTA's tiles (accumulate: not an item's first)
       auto product = [&](int t, bool accumulate) -> bool {
         const int st = t % S, pb = t & 1;
-        if (!mbar_wait(bar(Lay::bPFull + pb), static_cast<uint32_t>(t >> 1) & 1, abort_flag))
+        if (!warp_wait(bar(Lay::bPFull + pb), static_cast<uint32_t>(t >> 1) & 1, abort_flag))
           return false;
         tc_fence_after();
-        const uint64_t dv = sdesc_sw128(sbase + st * Lay::kStageBytes, Lay::kChunkBytes, 1024);
-        const uint64_t dp = sdesc_sw128(sbase + Lay::kP + pb * Lay::kPBytes, 16, 1024);
+        const SmemDesc dv = smem_desc(sbase + st * Lay::kStageBytes, Lay::kChunkBytes, 1024);
+        const SmemDesc dp = smem_desc(sbase + Lay::kP + pb * Lay::kPBytes, 16, 1024);
 #pragma unroll
         for (int k = 0; k < kKeyTile / 16; ++k)
-          mma_ss(tmem + Lay::tO, sdesc_advance(dv, k * 2048),
-                 sdesc_advance(dp, (k >> 2) * Lay::kQChunk + (k & 3) * 32), id_o,
-                 (accumulate || k > 0) ? 1u : 0u);
-        mma_commit(bar(Lay::bEmpty + st));
-        mma_commit(bar(Lay::bDone + pb));
+          warp_mma_ss(tmem + Lay::tO, dv, k * 2048, dp, (k >> 2) * Lay::kQChunk + (k & 3) * 32,
+                      id_o, (accumulate || k > 0) ? 1u : 0u);
+        warp_mma_commit(bar(Lay::bEmpty + st));
+        warp_mma_commit(bar(Lay::bDone + pb));
         return true;
       };
       int it = 0, item = 0;
       bool last_accumulates = false;
-      while (ok && ring.get(&w, &ok, abort_flag)) {
-        ring.read(true);
-        if (w.j0 >= w.j1) continue;
+      while (ok && __all_sync(0xffffffffu, ring.get(&w, &ok, abort_flag))) {
+        ring.read(lane == 0);
+        const int j0 = __shfl_sync(0xffffffffu, w.j0, 0), j1 = __shfl_sync(0xffffffffu, w.j1, 0);
+        if (j0 >= j1) continue;
         const int qb = item & 1;
-        ok = mbar_wait(bar(Lay::bQFull + qb), static_cast<uint32_t>(item >> 1) & 1, abort_flag);
-        const uint64_t dq = sdesc_sw128(sbase + Lay::kQ + qb * Lay::kQBytes, 16, 1024);
-        for (int j = w.j0; ok && j < w.j1; ++j, ++it) {
+        ok = warp_wait(bar(Lay::bQFull + qb), static_cast<uint32_t>(item >> 1) & 1, abort_flag);
+        const SmemDesc dq = smem_desc(sbase + Lay::kQ + qb * Lay::kQBytes, 16, 1024);
+        for (int j = j0; ok && j < j1; ++j, ++it) {
           const int st = it % S;
-          ok = mbar_wait(bar(Lay::bFull + st), static_cast<uint32_t>(it / S) & 1, abort_flag);
+          ok = warp_wait(bar(Lay::bFull + st), static_cast<uint32_t>(it / S) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t dk =
-              sdesc_sw128(sbase + st * Lay::kStageBytes + Lay::kTileBytes, 16, 1024);
+          const SmemDesc dk =
+              smem_desc(sbase + st * Lay::kStageBytes + Lay::kTileBytes, 16, 1024);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + (it & 1) * NQ,
-                   sdesc_advance(dk, (k >> 2) * Lay::kChunkBytes + (k & 3) * 32),
-                   sdesc_advance(dq, (k >> 2) * Lay::kQChunk + (k & 3) * 32), id_s,
-                   k > 0 ? 1u : 0u);
-          mma_commit(bar(Lay::bSFull + (it & 1)));
-          if (j == w.j1 - 1) mma_commit(bar(Lay::bQEmpty + qb));
+            warp_mma_ss(tmem + (it & 1) * NQ, dk, (k >> 2) * Lay::kChunkBytes + (k & 3) * 32, dq,
+                        (k >> 2) * Lay::kQChunk + (k & 3) * 32, id_s, k > 0 ? 1u : 0u);
+          warp_mma_commit(bar(Lay::bSFull + (it & 1)));
+          if (j == j1 - 1) warp_mma_commit(bar(Lay::bQEmpty + qb));
           if (it > 0) ok = product(it - 1, last_accumulates);
-          last_accumulates = j > w.j0;
+          last_accumulates = j > j0;
         }
         ++item;
       }
