@@ -76,7 +76,8 @@ int launch_rope(fa::RopeArgs& a, bool interleaved, int dtype, cudaStream_t strea
   if (blocks >= (1L << 31)) return FA_ERR_UNSUPPORTED;
   const size_t smem = static_cast<size_t>(a.tokens_per_block) * a.rot * sizeof(float);
   const dim3 grid(static_cast<unsigned>(blocks));
-  return launch(dtype == FA_BF16 ? fa::fa_rope_kernel<PAGED, true> : fa::fa_rope_kernel<PAGED, false>,
+  return launch(dtype == FA_BF16 ? fa::fa_rope_kernel<PAGED, true>
+                                 : fa::fa_rope_kernel<PAGED, false>,
                 grid, fa::kRopeThreads, smem, stream, a, interleaved);
 }
 
@@ -178,8 +179,12 @@ bool make_part_tmap(CUtensorMap* map, const float* ptr, int d, int rows) {
 // A stride of 0 over more than one row would alias rows of a tensor map.
 bool steps(long long stride, long long rows) { return rows <= 1 || stride > 0; }
 
-// Rows (tokens x query heads of a key head) that the step kernel takes for one pass.
-constexpr int kStepMaxRows = 64;
+// Rows (tokens x query heads of a key head) that the step kernel takes for one pass; the
+// chunk kernel takes more. 24 sequences with 500 to 8000 keys, 32 heads over 8, step and
+// chunk: 17-20 rows 59 and 66 us at d = 128, 20-32 rows 63 and 54 us at d = 64 (a tile there
+// has half the bytes and the same softmax); 36-64 rows 94 and 72 us at d = 128, 88 and 58
+// at d = 64, with a step kernel of 64 columns that these figures took out.
+int step_max_rows(int d) { return d == 128 ? 32 : 16; }
 
 // Workspace: a PartInfo per CTA, then base-2 log-sum-exps and normalised outputs (fp32) of
 // two parts per CTA, `rows` rows each.
@@ -190,7 +195,7 @@ struct Workspace {
 Workspace workspace_for(int max_q, int group, int d) {
   Workspace w;
   const long long rows = static_cast<long long>(max_q) * group;
-  w.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= kStepMaxRows ? 64 : 256;
+  w.rows = rows <= 16 ? 16 : rows <= step_max_rows(d) ? 32 : fa::kChunkRows;
   w.l_at = kGrid * sizeof(fa::PartInfo);
   w.o_at = w.l_at + 2ull * kGrid * w.rows * sizeof(float);
   w.bytes = w.o_at + 2ull * kGrid * w.rows * d * sizeof(float);
@@ -247,8 +252,11 @@ bool allow_smem(Kernel kernel, size_t smem) {
                               static_cast<int>(smem)) == cudaSuccess;
 }
 
-// The least cost (in key tiles) that is worth a CTA of its own.
-constexpr int kStepLeast = 2;
+// The least cost (in key tiles, kItemCost of them for an item) that is worth a CTA of its
+// own: one token over 1000 keys (32 heads over 8) takes 9.2 / 9.5 / 9.9 / 10.7 / 13.3 us
+// with 1 / 2 / 3 / 4 / 8, over 4000 keys 11.2 / 10.7 / 10.8 / 11.2 / 13.6, a prompt of 300
+// tokens 18.2 / 21.5 / 25.4 / 30.3 with 2 / 4 / 6 / 8.
+constexpr int kLeastCost = 2;
 
 template <int D, int NQ, bool BF16>
 int launch_step(const AttentionArgs& a) {
@@ -260,13 +268,10 @@ int launch_step(const AttentionArgs& a) {
   if (!make_maps(a, a.max_q, &q, &k, &v)) return FA_ERR_CUDA;
   const int st = launch(kern, dim3(kGrid), Lay::kThreads, Lay::kBytes, a.stream, q, k, v,
                         view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L, a.opart(),
-                        a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kStepLeast,
+                        a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kLeastCost,
                         a.scale * kLog2e);
   return st != FA_OK ? st : launch_merge<D, BF16>(a, a.max_q, 2);
 }
-
-// ... and for chunks, whose tiles take longer and whose parts are larger.
-constexpr int kChunkLeast = 4;
 
 template <int D, bool BF16>
 int launch_chunk(const AttentionArgs& a) {
@@ -295,7 +300,7 @@ int launch_chunk(const AttentionArgs& a) {
     return FA_ERR_CUDA;
   const int st = launch(kern, dim3(kGrid), fa::kChunkThreads, Lay::kSmem, a.stream, q, k, v,
                         o, part, view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L,
-                        a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kChunkLeast,
+                        a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kLeastCost,
                         a.scale * kLog2e);
   return st != FA_OK ? st : launch_merge<D, BF16>(a, tpt, 8);
 }
@@ -304,10 +309,11 @@ template <int D, bool BF16>
 int launch_attention(const AttentionArgs& a) {
   switch (a.ws.rows) {
     case 16: return launch_step<D, 16, BF16>(a);
-    case 32: return launch_step<D, 32, BF16>(a);
-    case 64: return launch_step<D, 64, BF16>(a);
-    default: return launch_chunk<D, BF16>(a);
+    case 32:
+      if constexpr (D == 128) return launch_step<D, 32, BF16>(a);
+      break;
   }
+  return launch_chunk<D, BF16>(a);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
 // fa_paged_step.cuh -- attention of a few new tokens per sequence over a paged cache: the
-// decode step and the check of drafted tokens (up to 64 rows per key head, a row being one
+// decode step and the check of drafted tokens (up to 32 rows per key head, a row being one
 // token's query head).
 //
 // The pass is bound by reading K and V from HBM once: with R rows it does 4 R d
@@ -18,18 +18,17 @@
 // so all query heads that share a key head share one pass over it. Columns beyond the
 // item's rows hold whatever lies in shared memory: a column's values meet no other's.
 //
-// Softmax: thread r of a warpgroup owns key r of the tile and 16 or 32 query columns. The
-// reference m of a column moves only when a score exceeds it by more than 2^8; whether
-// any does is one barrier-vote per tile, and only then are the tile's maxima exchanged and
-// O^T rescaled. Columns beyond the item's rows are skipped in fours. Two sums per column: of the 16-bit weights, which normalises O, and of the
-// unrounded ones, which gives L.
+// Softmax: thread r owns key r of the tile and all query columns. The reference m of a
+// column moves only when a score exceeds it by more than 2^8; whether any does is one
+// barrier-vote per tile, and only then are the tile's maxima exchanged and O^T rescaled.
+// Columns beyond the item's rows are skipped in fours. Two sums per column: of the 16-bit
+// weights, which normalises O, and of the unrounded ones, which gives L.
 //
 // V rows of keys that no row of the item sees -- behind the sequence's end, before its
 // window, or in pages that are not loaded -- are zeroed in shared memory, since 0 times
 // whatever an unwritten row holds need not be 0.
 //
-// Warps: 4 (NQ <= 32) or 8 (NQ = 64) softmax warps, two TMA producers (Q and K, V), the MMA
-// issuer, the scheduler.
+// Warps: four softmax warps, two TMA producers (Q and K, V), the MMA issuer, the scheduler.
 #pragma once
 
 #include "fa_paged_split.cuh"
@@ -40,14 +39,12 @@ constexpr float kStepRescaleSlack = 8.0f;
 
 template <int D, int NQ>
 struct StepLayout {
-  static constexpr int kGroups = NQ == 64 ? 2 : 1;  // softmax warpgroups
-  static constexpr int kCols = NQ / kGroups;        // query columns of a softmax thread
-  static constexpr int kSoftmax = 128 * kGroups;
+  static constexpr int kSoftmax = 128;
   static constexpr int kThreads = kSoftmax + 128;
   static constexpr uint32_t kTileBytes = kKeyTile * D * 2;
   static constexpr uint32_t kChunkBytes = kKeyTile * 128;  // 128 rows x 64 values
   static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // V tile, then K tile
-  static constexpr int kStages = (D == 128 ? 3 : 6) - (NQ == 64 ? (D == 128 ? 1 : 2) : 0);
+  static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr uint32_t kQChunk = NQ * 128;  // NQ rows x 64 values
   static constexpr uint32_t kQBytes = kQChunk * (D / 64);
   static constexpr uint32_t kPBytes = NQ * 256;  // NQ rows x 128 keys
@@ -65,7 +62,7 @@ struct StepLayout {
   static constexpr uint32_t kBytes = kAbort + 8 + 1024;
   // TMEM: S^T buffers at 0 and NQ, O^T at 2 NQ
   static constexpr uint32_t tO = 2 * NQ;
-  static constexpr uint32_t kTmemCols = NQ == 16 ? 64 : NQ == 32 ? 128 : 256;
+  static constexpr uint32_t kTmemCols = NQ == 16 ? 64 : 128;
   // barriers
   static constexpr int bFull = 0, bEmpty = kStages, bQFull = 2 * kStages, bQEmpty = bQFull + 2,
                        bSFull = bQEmpty + 2, bPFull = bSFull + 2,
@@ -136,7 +133,7 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
                          int least, float scale_log2) {
   using Lay = StepLayout<D, NQ>;
   constexpr int S = Lay::kStages;
-  constexpr int C = Lay::kCols;
+  constexpr int C = NQ;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t pad = ((raw_base + 1023u) & ~1023u) - raw_base;
@@ -294,24 +291,22 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
     }
   } else {
     // ----------------------------------------------------------------- softmax
-    const int wg = warp >> 2;         // columns wg * C .. wg * C + C - 1
-    const int r = threadIdx.x & 127;  // key of the tile = TMEM lane
-    const int q0 = wg * C;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    float* red = reinterpret_cast<float*>(smem + Lay::kRed) + q0 * 4;
-    float* sums = reinterpret_cast<float*>(smem + Lay::kSums) + q0 * 8;
-    float* refs = reinterpret_cast<float*>(smem + Lay::kRef) + q0;
-    const int gbar = 1 + wg;
+    const int r = threadIdx.x;  // key of the tile = TMEM lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    float* red = reinterpret_cast<float*>(smem + Lay::kRed);
+    float* sums = reinterpret_cast<float*>(smem + Lay::kSums);
+    float* refs = reinterpret_cast<float*>(smem + Lay::kRef);
+    constexpr int gbar = 1;  // the softmax warps' named barrier
     // a column that has seen no key: below every finite score, and -inf - kNone = -inf
     constexpr float kNone = -3.402823466e38f;
     int it = 0;
     while (true) {
       const bool more = ring.get(&w, &ok, abort_flag);
       __syncwarp();
-      // all of the group leave together; and the last item's sums have been read
+      // all leave together; and the last item's sums have been read
       if (!named_bar_and(gbar, 128, more)) break;
       ring.read(lane == 0);
-      const int cols = min(C, w.n * group - q0);  // of this warpgroup, at least 1 in group 0
+      const int cols = w.n * group;
       const int off = w.nk - w.n;
       // keys that every row sees
       const int all_lo = w.n - 1 + off - wl, all_hi = min(w.nk - 1, off + wr);
@@ -332,7 +327,7 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
         if (ok) {
           tc_fence_after();
           uint32_t sr[C];
-          tmem_ld_cols<C>(lane_base + b * NQ + q0, sr);
+          tmem_ld_cols<C>(lane_base + b * NQ, sr);
 #pragma unroll
           for (int q = 0; q < C; ++q) s[q] = __uint_as_float(sr[q]);
           if (key0 < all_lo || key0 + kKeyTile - 1 > all_hi) {  // an edge of the mask
@@ -340,10 +335,10 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < C; ++q) {
               if ((q & 3) == 0 && q >= cols) break;
-              const int mid = tok[q0 + q] + off;
+              const int mid = tok[q] + off;
               if (key > min(w.nk - 1, mid + wr) || key < mid - wl) s[q] = -INFINITY;
             }
-            if (wg == 0 && (key < w.keys.lo || key > w.keys.hi)) {
+            if (key < w.keys.lo || key > w.keys.hi) {
               const uint32_t v = sbase + (it % S) * Lay::kStageBytes + r * 128;
               // the stage has landed: its K has been multiplied
 #pragma unroll
@@ -368,7 +363,7 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < C; ++q) v[q] = s[q];
             const float top = reduce_columns<C>(v, lane, MaxOf());
-            if (lane < C) red[lane * 4 + (warp & 3)] = top * scale_log2;
+            if (lane < C) red[lane * 4 + warp] = top * scale_log2;
           }
           named_bar_sync(gbar, 128);
           // O^T holds products: it is rescaled, once the last of them has landed
@@ -396,8 +391,8 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
             }
             if (rescale && ok) {
               uint32_t o[4];
-              tmem_ld4(lane_base + Lay::tO + q0 + q4, o);
-              tmem_st4(lane_base + Lay::tO + q0 + q4,
+              tmem_ld4(lane_base + Lay::tO + q4, o);
+              tmem_st4(lane_base + Lay::tO + q4,
                        __float_as_uint(__uint_as_float(o[0]) * alpha[0]),
                        __float_as_uint(__uint_as_float(o[1]) * alpha[1]),
                        __float_as_uint(__uint_as_float(o[2]) * alpha[2]),
@@ -421,7 +416,7 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
           unpack2<BF16>(pk, pr, unused);
           l[q] += p;
           l_o[q] += pr;
-          *reinterpret_cast<uint16_t*>(pt + step_swz<NQ>(q0 + q, r)) =
+          *reinterpret_cast<uint16_t*>(pt + step_swz<NQ>(q, r)) =
               static_cast<uint16_t>(pk & 0xFFFFu);
         }
         fence_async_smem();
@@ -434,8 +429,8 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
         const float a = reduce_columns<C>(l, lane, SumOf());
         const float e = reduce_columns<C>(l_o, lane, SumOf());
         if (lane < C) {
-          sums[lane * 8 + (warp & 3)] = a;
-          sums[lane * 8 + 4 + (warp & 3)] = e;
+          sums[lane * 8 + warp] = a;
+          sums[lane * 8 + 4 + warp] = e;
         }
         if (r == 0) {
 #pragma unroll
@@ -456,7 +451,7 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
 #pragma unroll 1
       for (int q4 = 0; q4 < cols; q4 += 4) {
         uint32_t o[4];
-        tmem_ld4(lane_base + Lay::tO + q0 + q4, o);
+        tmem_ld4(lane_base + Lay::tO + q4, o);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int q = q4 + k;
@@ -466,12 +461,12 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
           // no key seen: O = 0 (and O^T may not have been written at all)
           const float val = e > 0.f ? __fdividef(__uint_as_float(o[k]), e) : 0.f;
           if (whole) {
-            const int tq = tok[q0 + q];
-            const int head = w.h * group + q0 + q - tq * group;
+            const int tq = tok[q];
+            const int head = w.h * group + q - tq * group;
             O[(w.begin + tq) * so.sn + head * so.sh + r] =
                 static_cast<uint16_t>(pack2<BF16>(val, 0.f) & 0xFFFFu);
           } else {
-            Opart[(slot * NQ + q0 + q) * D + r] = val;
+            Opart[(slot * NQ + q) * D + r] = val;
           }
         }
       }
@@ -481,12 +476,12 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
         const float a = (t.x + t.y) + (t.z + t.w);
         const float L2 = a > 0.f ? refs[r] + log2f(a) : -INFINITY;
         if (whole) {
-          const int tq = tok[q0 + r];
-          const int head = w.h * group + q0 + r - tq * group;
+          const int tq = tok[r];
+          const int head = w.h * group + r - tq * group;
           L[static_cast<long>(head) * c.tokens + w.begin + tq] =
               L2 * 0.69314718055994530942f;
         } else {
-          Lpart[slot * NQ + q0 + r] = L2;
+          Lpart[slot * NQ + r] = L2;
         }
       }
       tc_fence_before();

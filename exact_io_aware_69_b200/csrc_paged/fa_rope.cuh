@@ -10,8 +10,8 @@
 // The pass is bound by HBM: every element is read and written once. So a block takes a few
 // tokens and computes their rot_dim / 2 sines and cosines once into shared memory (a token's
 // angles serve all its heads; per thread and head they would cost more instructions than
-// the rotation); its threads then stream rows: a thread owns two 16-byte vectors of a row, half the rotated (or half the copied) columns
-// apart, so that in the half form it holds both columns of its pairs, neighbouring threads
+// the rotation); its threads then stream rows: a thread owns two 16-byte vectors of a row,
+// half the rotated (or half the copied) columns apart, so that in the half form it holds both columns of its pairs, neighbouring threads
 // hold neighbouring vectors in both forms, and every store covers whole sectors; it keeps
 // its angles in registers over the heads of its token. Threads of a warp run over the
 // heads of a token or over tokens, whichever lie closer together in memory.
@@ -201,9 +201,9 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a,
         const RopeRows& rows = r < nq ? a.q : r < nk ? a.k : a.v;
         const int h = r < nq ? r : r < nk ? r - nq : r - nk;
         // append: K and V rows go to row s_row of page s_page (sb: the page stride)
-        uint16_t* dst = PAGED && r >= nq ? rows.dst + s_page[ti] * rows.sd.sb + h * rows.sd.sh +
-                                               s_row[ti] * rows.sd.sn
-                                         : rows.dst + b * rows.sd.sb + h * rows.sd.sh + n * rows.sd.sn;
+        const bool paged = PAGED && r >= nq;
+        uint16_t* dst = rows.dst + (paged ? s_page[ti] : b) * rows.sd.sb + h * rows.sd.sh +
+                        (paged ? s_row[ti] : n) * rows.sd.sn;
         *reinterpret_cast<uint4*>(dst + c0) = x[u];
         *reinterpret_cast<uint4*>(dst + c1) = y[u];
       }

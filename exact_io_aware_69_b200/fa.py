@@ -89,7 +89,8 @@ _NO_ROWS = (0,) * 9
 
 _lib = None
 _paged_lib = None
-_torch = _raw_stream = None  # set with _paged_lib: a call's own import and lookup cost more
+# set with _paged_lib: an import and lookups in every call cost a microsecond
+_torch = _raw_stream = _codes = None
 
 
 class FaError(RuntimeError):
@@ -109,10 +110,11 @@ def load():
 
 def load_paged():
     """Load libfa_paged.so (raises if it has not been built)."""
-    global _paged_lib, _torch, _raw_stream
+    global _paged_lib, _torch, _raw_stream, _codes
     if _paged_lib is None:
         import torch
         _torch = torch
+        _codes = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16}
         # the current stream's handle without building a Stream object, where torch has it
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -372,10 +374,12 @@ def _pack(fields, *values):
         raise _bad(str(e)) from None
 
 
-def _on_stream(stream, call, *args):
-    """call(*args) with `stream` (and its device) as the current one, so that what the call
-    allocates belongs to it."""
+def _on_stream(stream, like, call, *args):
+    """call(*args) with `stream` as the current one, so that what the call allocates belongs
+    to it."""
     import torch
+    if stream.device_index != like.get_device():
+        raise _bad("the stream is not of the tensors' device")
     with torch.cuda.stream(stream):
         return call(*args)
 
@@ -424,12 +428,14 @@ def _check_freqs(freqs, device):
 
 def _rope(q, k, freqs, positions, magnitude, interleaved, layout, q_out, k_out, stream, inverse):
     if stream is not None:
-        return _on_stream(stream, _rope, q, k, freqs, positions, magnitude, interleaved, layout,
+        return _on_stream(stream, q, _rope, q, k, freqs, positions, magnitude, interleaved, layout,
                           q_out, k_out, None, inverse)
     lib = _paged_lib or load_paged()
     torch = _torch
     dtype = q.dtype
-    code = _dtype_code(q)
+    code = _codes.get(dtype)
+    if code is None:
+        raise FaError(FA_ERR_UNSUPPORTED, f"dtype {dtype}")
     device = _place(q, "q")
     if device != torch.cuda.current_device():
         with torch.cuda.device(device):
@@ -485,8 +491,10 @@ def rope_backward(dq, dk, freqs, positions=None, magnitude: float = 1.0,
 
 def _paged_cache(x, name, device, k_pages, v_pages, page_table, cu_q, seq_k, page_layout):
     """The fields of the fa_paged_cache of these tensors for the packed rows x [T, H, d]."""
-    code = _dtype_code(x)
     dtype, i32 = x.dtype, _torch.int32
+    code = _codes.get(dtype)
+    if code is None:
+        raise FaError(FA_ERR_UNSUPPORTED, f"dtype {dtype}")
     if x.dim() != 3:
         raise _bad(f"{name} is not a packed [T, H, d] tensor")
     if k_pages.get_device() != device or v_pages.get_device() != device or \
@@ -528,8 +536,8 @@ def paged_append(k, v, k_pages, v_pages, page_table, cu_q, seq_k, q=None, freqs=
     the way as in rope(), each at its position in the sequence (or at positions [T]), and so
     is q [T, Hq, d], if given; returns the rotated q (q_out, which may be q), or None."""
     if stream is not None:
-        return _on_stream(stream, paged_append, k, v, k_pages, v_pages, page_table, cu_q, seq_k, q,
-                          freqs, magnitude, interleaved, positions, q_out, page_layout)
+        return _on_stream(stream, k, paged_append, k, v, k_pages, v_pages, page_table, cu_q, seq_k,
+                          q, freqs, magnitude, interleaved, positions, q_out, page_layout)
     lib = _paged_lib or load_paged()
     torch = _torch
     device = _place(k, "k")
@@ -581,7 +589,7 @@ def paged_attention(q, k_pages, v_pages, page_table, cu_q, seq_k, max_q: int | N
     seq_k keys; here `causal` is the default. max_q: the most new tokens that any sequence
     has (None: T); 1 for a decode step. Rows behind the last sequence are not written."""
     if stream is not None:
-        return _on_stream(stream, paged_attention, q, k_pages, v_pages, page_table, cu_q, seq_k,
+        return _on_stream(stream, q, paged_attention, q, k_pages, v_pages, page_table, cu_q, seq_k,
                           max_q, causal, scale, window, page_layout, out, lse, workspace)
     lib = _paged_lib or load_paged()
     torch = _torch

@@ -164,10 +164,10 @@ def test_null_arguments(lib):
 
 
 def test_workspace_size(lib):
-    """Two parts per CTA (148) of 16, 32, 64 or 256 rows, d outputs and a log-sum-exp each,
-    behind 32 bytes per CTA."""
-    for max_q, hq, heads, d, rows in ((1, 8, 8, 64, 16), (4, 32, 8, 128, 16), (5, 32, 8, 64, 32),
-                                      (64, 2, 2, 128, 64), (65, 2, 2, 128, 256)):
+    """Two parts per CTA (148) of 16, 32 or 256 rows, d outputs and a log-sum-exp each, behind
+    32 bytes per CTA."""
+    for max_q, hq, heads, d, rows in ((1, 8, 8, 64, 16), (4, 32, 8, 128, 16), (5, 32, 8, 128, 32),
+                                      (5, 32, 8, 64, 256), (33, 2, 2, 128, 256)):
         assert lib.fa_paged_workspace_size(1000, max_q, hq, heads, d) == \
             148 * 32 + 2 * 148 * rows * (d + 1) * 4
     assert lib.fa_paged_workspace_size(0, 1, 8, 2, 128) == 0
@@ -177,8 +177,7 @@ def test_workspace_size(lib):
 
 
 # Threads per block of every kernel the library launches.
-# (fa_paged_step_kernel: 192 up to 32 query columns, 320 for 64)
-BLOCK_THREADS = {"fa_rope_kernel": 128, "fa_paged_step_kernel": 192, "fa_paged_merge_kernel": 256,
+BLOCK_THREADS = {"fa_rope_kernel": 128, "fa_paged_step_kernel": 256, "fa_paged_merge_kernel": 256,
                  "fa_paged_chunk_kernel": 384}
 
 
@@ -188,8 +187,7 @@ def test_every_kernel_fits_the_register_file_at_its_block_size():
         fam = [k for k in BLOCK_THREADS if k in name]
         assert len(fam) == 1, name
         seen.add(fam[0])
-        wide = re.search(r"fa_paged_step_kernelILi\d+ELi64E", name)
-        warps = -(-(320 if wide else BLOCK_THREADS[fam[0]]) // 32)
+        warps = -(-BLOCK_THREADS[fam[0]] // 32)
         regs = -(-res["registers"] // 8) * 8  # allocated in units of 8 per thread
         assert regs * 32 * -(-warps // 4) <= 16384, (name, res["registers"])
     assert seen == set(BLOCK_THREADS)
