@@ -588,8 +588,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                            mbar_wait(bar(Lay::bDone + 2 * g + 1), (used - 1) & 1, abort_flag))));
       tc_fence_after();
       // rows that see no key: O = 0, L = -inf (their sums need not be 0: the polynomial's
-      // least value is 2^-125)
-      const bool none = m == -INFINITY;
+      // least value is 2^-125); a NaN among the scores shows in the sum and stays one
+      const bool none = m == -INFINITY && l == l;
       float L2 = none ? -INFINITY : m + log2f(l);
       float inv_l = none ? 0.f : 1.f / l;
       float inv_other = 0.f;

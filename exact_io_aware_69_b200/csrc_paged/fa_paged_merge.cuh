@@ -135,21 +135,20 @@ __global__ void __launch_bounds__(kMergeThreads)
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < CPL; ++i) o[i] = 0.f;
-        if (top != -INFINITY) {
+        const float from = top == -INFINITY ? 0.f : top;
 #pragma unroll
-          for (int i = 0; i < kMergeWarps; ++i) {
-            const float f = ex2_approx(s_m[i] - top);
-            sum = fmaf(f, s_l[i], sum);
+        for (int i = 0; i < kMergeWarps; ++i) {
+          const float f = ex2_approx(s_m[i] - from);
+          sum = fmaf(f, s_l[i], sum);
 #pragma unroll
-            for (int k = 0; k < CPL; ++k) o[k] = fmaf(f, s_o[i][lane * CPL + k], o[k]);
-          }
+          for (int k = 0; k < CPL; ++k) o[k] = fmaf(f, s_o[i][lane * CPL + k], o[k]);
         }
         M = top;
         tot = sum;
       }
     }
     if (!shared_row || warp == 0) {
-      const float inv = tot > 0.f ? 1.f / tot : 0.f;
+      const float inv = tot == 0.f ? 0.f : 1.f / tot;
       const int head_q = item.y * group + q;
       uint16_t* dst = O + (item.x + t) * so.sn + head_q * so.sh + lane * CPL;
       if constexpr (CPL == 4)
@@ -159,7 +158,7 @@ __global__ void __launch_bounds__(kMergeThreads)
         *reinterpret_cast<uint32_t*>(dst) = pack2<BF16>(o[0] * inv, o[1] * inv);
       if (lane == 0)
         L[static_cast<long>(head_q) * tokens + item.x + t] =
-            tot > 0.f ? (M + log2f(tot)) * 0.69314718055994530942f : -INFINITY;
+            tot == 0.f ? -INFINITY : (M + log2f(tot)) * 0.69314718055994530942f;
     }
     // (a shared row is its block's only one: s_m, s_l and s_o are written once)
   }

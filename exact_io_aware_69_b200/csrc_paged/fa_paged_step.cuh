@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
           const float4 t = *reinterpret_cast<const float4*>(sums + q * 8 + 4);
           const float e = (t.x + t.y) + (t.z + t.w);
           // no key seen: O = 0 (and O^T may not have been written at all)
-          const float val = e > 0.f ? __fdividef(__uint_as_float(o[k]), e) : 0.f;
+          const float val = e == 0.f ? 0.f : __fdividef(__uint_as_float(o[k]), e);
           if (whole) {
             const int tq = tok[q];
             const int head = w.h * group + q - tq * group;
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
       if (r < cols) {
         const float4 t = *reinterpret_cast<const float4*>(sums + r * 8);
         const float a = (t.x + t.y) + (t.z + t.w);
-        const float L2 = a > 0.f ? refs[r] + log2f(a) : -INFINITY;
+        const float L2 = a == 0.f ? -INFINITY : refs[r] + log2f(a);
         if (whole) {
           const int tq = tok[r];
           const int head = w.h * group + r - tq * group;

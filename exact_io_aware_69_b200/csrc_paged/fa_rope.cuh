@@ -11,10 +11,11 @@
 // tokens and computes their rot_dim / 2 sines and cosines once into shared memory (a token's
 // angles serve all its heads; per thread and head they would cost more instructions than
 // the rotation); its threads then stream rows: a thread owns two 16-byte vectors of a row,
-// half the rotated (or half the copied) columns apart, so that in the half form it holds both columns of its pairs, neighbouring threads
-// hold neighbouring vectors in both forms, and every store covers whole sectors; it keeps
-// its angles in registers over the heads of its token. Threads of a warp run over the
-// heads of a token or over tokens, whichever lie closer together in memory.
+// half the rotated (or half the copied) columns apart, so that in the half form it holds
+// both columns of its pairs, neighbouring threads hold neighbouring vectors in both forms,
+// and every store covers whole sectors; it keeps its angles in registers over the heads of
+// its token. Threads of a warp run over the heads of a token or over tokens, whichever lie
+// closer together in memory.
 //
 // Small blocks and two rows in flight per thread keep 2048 threads on an SM, which is what
 // carries the bandwidth: 2 x 8192 tokens of 32 + 8 heads, d 128, bf16 (336 MB) take 55.4 us
@@ -173,42 +174,48 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a,
     sines[i] = s * a.magnitude * a.sign;
   }
   __syncthreads();
-  if (!active || (PAGED && s_owner[ti] < 0)) return;
-
-  float cs[8], sn[8];
-  if (turns) {
-    // pairs of the first vector and of the second: the same eight, or four and four
-    const float* c = cosines + ti * half + (interleaved ? 4 * g : 8 * g);
-    const float* s = sines + ti * half + (interleaved ? 4 * g : 8 * g);
-    const int second = interleaved ? half / 2 : 4;
+  if (active && (!PAGED || s_owner[ti] >= 0)) {
+    float cs[8], sn[8];
+    if (turns) {
+      // pairs of the first vector and of the second: the same eight, or four and four
+      const float* c = cosines + ti * half + (interleaved ? 4 * g : 8 * g);
+      const float* s = sines + ti * half + (interleaved ? 4 * g : 8 * g);
+      const int second = interleaved ? half / 2 : 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      cs[i] = c[i];
-      sn[i] = s[i];
-      cs[4 + i] = c[second + i];
-      sn[4 + i] = s[second + i];
+      for (int i = 0; i < 4; ++i) {
+        cs[i] = c[i];
+        sn[i] = s[i];
+        cs[4 + i] = c[second + i];
+        sn[4 + i] = s[second + i];
+      }
     }
-  }
-  // rows of K and V whose page is not valid are not written
-  const int last = PAGED && s_page[ti] < 0 ? nq : total;
-  for (int r0 = rl; r0 < last; r0 += kRopeRows * rlanes) {
-    fetch(r0);
+    // rows of K and V whose page is not valid are not written
+    const int last = PAGED && s_page[ti] < 0 ? nq : total;
+    for (int r0 = rl; r0 < last; r0 += kRopeRows * rlanes) {
+      fetch(r0);
 #pragma unroll
-    for (int u = 0; u < kRopeRows; ++u) {
-      const int r = r0 + u * rlanes;
-      if (r < last) {
-        if (turns && r < nk) rotate16<BF16>(x[u], y[u], cs, sn, interleaved);
-        const RopeRows& rows = r < nq ? a.q : r < nk ? a.k : a.v;
-        const int h = r < nq ? r : r < nk ? r - nq : r - nk;
-        // append: K and V rows go to row s_row of page s_page (sb: the page stride)
-        const bool paged = PAGED && r >= nq;
-        uint16_t* dst = rows.dst + (paged ? s_page[ti] : b) * rows.sd.sb + h * rows.sd.sh +
-                        (paged ? s_row[ti] : n) * rows.sd.sn;
-        *reinterpret_cast<uint4*>(dst + c0) = x[u];
-        *reinterpret_cast<uint4*>(dst + c1) = y[u];
+      for (int u = 0; u < kRopeRows; ++u) {
+        const int r = r0 + u * rlanes;
+        if (r < last) {
+          if (turns && r < nk) rotate16<BF16>(x[u], y[u], cs, sn, interleaved);
+          const RopeRows& rows = r < nq ? a.q : r < nk ? a.k : a.v;
+          const int h = r < nq ? r : r < nk ? r - nq : r - nk;
+          // append: K and V rows go to row s_row of page s_page (sb: the page stride)
+          const bool paged = PAGED && r >= nq;
+          uint16_t* dst = rows.dst + (paged ? s_page[ti] : b) * rows.sd.sb + h * rows.sd.sh +
+                          (paged ? s_row[ti] : n) * rows.sd.sn;
+          *reinterpret_cast<uint4*>(dst + c0) = x[u];
+          *reinterpret_cast<uint4*>(dst + c1) = y[u];
+        }
       }
     }
   }
+  // lengths that no row led to
+  if (PAGED && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.cache.batch; i += kRopeThreads) {
+      const SeqInfo s = seq_info(a.cache, i, a.cache.tokens);
+      if (!s.ok || (s.n > 0 && s.n > s.nk)) atomicExch(&g_fa_status, kStatusInvalid);
+    }
 }
 
 }  // namespace fa

@@ -10,7 +10,7 @@ import pytest
 
 from exact_io_aware_69_b200 import fa
 
-from paged_cases import check, make_batch
+from paged_cases import check, make_batch, reference
 from test_gpu_rope import close, freqs_of, plain
 
 pytestmark = pytest.mark.gpu
@@ -60,6 +60,15 @@ ATTEND = [  # (lengths, hq, hkv, d, page, window)
     ([(60, 60)] * 9 + [(1, 800)] * 7, 5, 5, 64, 16, CAUSAL),
     ([(150, 700)], 128, 1, 64, 512, CAUSAL),
     ([(3, 20000)], 48, 1, 64, 64, CAUSAL),
+    ([(1, 1 + 37 * i % 700) for i in range(300)], 8, 2, 128, 16, CAUSAL),
+    ([(1, 1 + i % 5) for i in range(2100)], 2, 1, 64, 16, CAUSAL),
+    ([(1 + 29 * i % 211, 211 + 67 * i % 400) for i in range(70)], 4, 2, 64, 32, CAUSAL),
+    ([(200, 500), (1, 300)], 8, 2, 128, 64, (0, 0)),
+    ([(2, 500)], 8, 2, 128, 64, (0, 0)),
+    ([(130, 900)], 4, 4, 128, 128, (5, -1)),
+    ([(65, 400)], 2, 1, 64, 16, (-1, 40)),
+    ([(32, 600), (7, 7)], 1, 1, 128, 16, CAUSAL),
+    ([(17, 600), (1, 33)], 1, 1, 64, 16, CAUSAL),
 ]
 
 
@@ -286,6 +295,145 @@ def test_chunks_then_steps_equal_the_whole():
     ro, rl, _ = fa.forward(qr, *rep, causal=True, layout="bnhd", residual=False)
     assert (torch.cat(got_o).float() - ro[0].float()).abs().max() <= 4e-2
     assert (torch.cat(got_l, 1) - rl[0]).abs().max() <= 2e-3
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_lengths_that_do_not_fit(n):
+    """A sequence with more new tokens than max_q, and rows that cu_q gives to nobody."""
+    import torch
+    d = 128
+    batch = make_batch([(n, 300), (n + 2, 200), (n, 100)], 4, 2, d, 64, torch.bfloat16, seed=5)
+    want, wantL = fa.paged_attention(batch.q, *batch.cache, max_q=n + 2)
+    out = torch.full_like(batch.q, 7.0)
+    o, L = fa.paged_attention(batch.q, *batch.cache, max_q=n, out=out)
+    assert fa.device_status() == fa.FA_ERR_INVALID
+    rows = slice(n, 2 * n + 2)
+    assert (o[rows] == 7).all()
+    o[rows], L[:, rows] = want[rows], wantL[:, rows]
+    check(batch, o, L, d ** -0.5, CAUSAL)
+    for cu in ([0, n, n - 1, 3 * n + 2], [0, n, 2 * n + 2, 3 * n + 3], [-1, n, 2 * n + 2, 3 * n + 2]):
+        cu_q = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        fa.paged_attention(batch.q, batch.k_pages, batch.v_pages, batch.page_table, cu_q,
+                           batch.seq_k)
+        assert fa.device_status() == fa.FA_ERR_INVALID
+        k = torch.zeros(3 * n + 2, 2, d, device="cuda").bfloat16()
+        pools = [p.clone() for p in (batch.k_pages, batch.v_pages)]
+        fa.paged_append(k, k, *pools, batch.page_table, cu_q, batch.seq_k)
+        assert fa.device_status() == fa.FA_ERR_INVALID
+    # rows before the first sequence and between none: only the named ones are written
+    cu_q = torch.tensor([n, n, 2 * n + 2, 2 * n + 2], dtype=torch.int32, device="cuda")
+    out = torch.full_like(batch.q, 7.0)
+    o, L = fa.paged_attention(batch.q, batch.k_pages, batch.v_pages, batch.page_table, cu_q,
+                              batch.seq_k, out=out)
+    assert fa.device_status() == fa.FA_OK
+    assert (o[:n] == 7).all() and (o[2 * n + 2:] == 7).all()
+    ref = reference(batch, d ** -0.5, CAUSAL)[1]
+    assert ((o[rows].double() - ref[0]).abs() <= ref[2]).all()
+
+
+@pytest.mark.parametrize("n", [1, 50])
+def test_nan_reaches_its_rows_only(n):
+    """A NaN query, and a NaN in a key that only later tokens see: NaN where the definition
+    has it, the other rows as they are."""
+    import torch
+    d = 64
+    batch = make_batch([(n, 3000), (n, 700)], 4, 2, d, 64, torch.bfloat16, seed=7)
+    batch.q[n, 1, 3] = float("nan")
+    o, L = fa.paged_attention(batch.q, *batch.cache, max_q=n)
+    assert fa.device_status() == fa.FA_OK
+    bad = torch.zeros(2 * n, 4, dtype=torch.bool, device="cuda")
+    bad[n, 1] = True
+    assert torch.equal(o.isnan().all(-1), bad) and torch.equal(o.isnan().any(-1), bad)
+    assert torch.equal(L.isnan().T, bad)
+    batch.q[n, 1, 3] = 0.5
+    if n > 1:
+        at = 3000 - n + 20  # the key of new token 20
+        page = batch.page_table[0, at // 64].long()
+        old = batch.k_pages[page, at % 64, 0].clone()
+        batch.k_pages[page, at % 64, 0] = float("nan")
+        o, L = fa.paged_attention(batch.q, *batch.cache, max_q=n)
+        bad[:] = False
+        bad[20:n, :2] = True
+        assert torch.equal(o.isnan().any(-1), bad) and torch.equal(L.isnan().T, bad)
+        batch.k_pages[page, at % 64, 0] = old
+
+
+def test_a_pool_past_32_bit_offsets():
+    """Pages whose elements lie beyond 2^32: written and read in place."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 30 * 2**30:
+        pytest.skip("needs 20 GB of device memory")
+    page, hkv, d = 256, 16, 128
+    count = 2 * 2**32 // (2 * page * hkv * d) + 3
+    pool = torch.empty((count, 2, page, hkv, d), device="cuda", dtype=torch.bfloat16)
+    assert pool[-1, 1].storage_offset() > 2**32
+    kp, vp = pool[:, 0], pool[:, 1]
+    table = torch.tensor([[count - 1, 0, count - 2]], dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(600, hkv, d, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(600, 2 * hkv, d, device="cuda").bfloat16()
+    cu = torch.tensor([0, 600], dtype=torch.int32, device="cuda")
+    sk = torch.tensor([600], dtype=torch.int32, device="cuda")
+    fa.paged_append(k, v, kp, vp, table, cu, sk)
+    assert torch.equal(kp[count - 1], k[:256]) and torch.equal(vp[count - 2, :88], v[512:])
+    for rows in (600, 1):
+        q_ = q[600 - rows:]
+        cu = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+        o, L = fa.paged_attention(q_, kp, vp, table, cu, sk, max_q=rows)
+        assert fa.device_status() == fa.FA_OK
+        whole = make_batch([(rows, 600)], 2 * hkv, hkv, d, 256, torch.bfloat16)
+        whole.q, whole.keys, whole.values = q_, [k.cpu()], [v.cpu()]
+        check(whole, o, L, d ** -0.5, CAUSAL)
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed in turn, each gives what an eager call gives: a call leaves nothing in the
+    workspace that the next one reads."""
+    import torch
+    batches = [make_batch([(1, 5000), (1, 40)], 8, 2, 128, 16, torch.bfloat16, seed=1),
+               make_batch([(90, 3000)], 8, 2, 128, 64, torch.bfloat16, seed=2)]
+    wants = [fa.paged_attention(b.q, *b.cache, max_q=b.max_q) for b in batches]
+    size = max(fa.paged_workspace_size(b.q.shape[0], b.max_q, 8, 2, 128) for b in batches)
+    workspace = torch.full((size,), 255, device="cuda", dtype=torch.uint8)
+    graphs, outs = [], []
+    for b in batches:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(fa.paged_attention(b.q, *b.cache, max_q=b.max_q, workspace=workspace))
+        graphs.append(graph)
+    for _ in range(4):
+        for graph, out, want in zip(graphs, outs, wants):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_a_long_chain_of_dependent_calls():
+    """Rotated appends and attention back to back, each reading what the one before wrote
+    (launches overlap; reads must not), against the same calls one by one."""
+    import torch
+    torch.manual_seed(2)
+    freqs = freqs_of(64)
+
+    def chain(wait):
+        gen = torch.Generator("cuda").manual_seed(5)
+        kp, vp = (torch.zeros(70, 16, 2, 64, device="cuda").bfloat16() for _ in range(2))
+        table = torch.arange(70, device="cuda", dtype=torch.int32).view(2, 35)
+        x = torch.randn(2, 8, 64, device="cuda", generator=gen).bfloat16()
+        cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+        seen = []
+        for i in range(1, 300):
+            sk = torch.full((2,), i, dtype=torch.int32, device="cuda")
+            q = fa.paged_append(x[:, :2], x[:, 2:4], kp, vp, table, cu, sk, q=x, freqs=freqs)
+            if wait:
+                torch.cuda.synchronize()
+            o, _ = fa.paged_attention(q, kp, vp, table, cu, sk, max_q=1)
+            if wait:
+                torch.cuda.synchronize()
+            x, _ = fa.rope(o[None], None, freqs, layout="bnhd")
+            x = x[0]
+            seen.append(x)
+        return torch.stack(seen), kp, vp
+    assert all(torch.equal(a, b) for a, b in zip(chain(False), chain(True)))
 
 
 def test_attention_on_other_streams_at_once():
