@@ -70,7 +70,7 @@ int rope_tokens_per_block(long rows, int groups) {
 template <bool PAGED>
 int launch_rope(fa::RopeArgs& a, bool interleaved, int dtype, cudaStream_t stream) {
   a.tokens_per_block = rope_tokens_per_block(a.rows, a.d / 16);
-  const fa::RopeRows& most = a.q.heads > 0 ? a.q : a.k;
+  const fa::RopeRows& most = a.kinds[a.kinds[0].heads > 0 ? 0 : 1];
   a.tokens_first = most.ss.sn < most.ss.sh;
   const long blocks = (a.rows + a.tokens_per_block - 1) / a.tokens_per_block;
   if (blocks >= (1L << 31)) return FA_ERR_UNSUPPORTED;
@@ -332,8 +332,8 @@ int fa_rope(const fa_rope_args* args, void* stream) {
   if (static_cast<long long>(r.batch) * r.rows == 0 || r.q.heads + r.k.heads == 0) return FA_OK;
   if (!ok_rows(r.q) || !ok_rows(r.k) || !aligned(r.positions, 4)) return FA_ERR_INVALID;
   fa::RopeArgs a{};
-  a.q = rope_rows(r.q);
-  a.k = rope_rows(r.k);
+  a.kinds[0] = rope_rows(r.q);
+  a.kinds[1] = rope_rows(r.k);
   a.positions = r.positions;
   a.pos_row = static_cast<long>(r.pos_row);
   a.freqs = r.freqs;
@@ -363,9 +363,9 @@ int fa_paged_append(const fa_paged_append_args* args, void* stream) {
   if (c.num_pages == 0 || c.table_width == 0) return FA_ERR_INVALID;
   const fa_strides kp{c.k_page, c.k_head, c.k_row}, vp{c.v_page, c.v_head, c.v_row};
   fa::RopeArgs a{};
-  a.q = rope_rows(r.q);
-  a.k = rope_rows({r.k, c.k_pages, r.ks, kp, c.heads, 0});
-  a.v = rope_rows({r.v, c.v_pages, r.vs, vp, c.heads, 0});
+  a.kinds[0] = rope_rows(r.q);
+  a.kinds[1] = rope_rows({r.k, c.k_pages, r.ks, kp, c.heads, 0});
+  a.kinds[2] = rope_rows({r.v, c.v_pages, r.vs, vp, c.heads, 0});
   a.positions = r.positions;
   a.freqs = r.freqs;
   a.rot = r.freqs != nullptr ? r.rot_dim : 0;

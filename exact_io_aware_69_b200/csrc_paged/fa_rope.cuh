@@ -17,8 +17,7 @@
 // its token. Threads of a warp run over the heads of a token or over tokens, whichever lie
 // closer together in memory.
 //
-// Small blocks and two rows in flight per thread keep 2048 threads on an SM, which is what
-// carries the bandwidth: 2 x 8192 tokens of 32 + 8 heads, d 128, bf16 (336 MB) take 55.4 us
+// Small blocks and two rows in flight per thread carry the most bandwidth: 2 x 8192 tokens of 32 + 8 heads, d 128, bf16 (336 MB) take 55.4 us
 // (6.06 TB/s, 0.93 of the copy rate); 256 threads with 2 / 4 / 5 rows 56.2 / 57.6 / 65.2,
 // loading the first rows before the angles are there 57.7 to 65.
 #pragma once
@@ -40,7 +39,7 @@ struct RopeRows {
 };
 
 struct RopeArgs {
-  RopeRows q, k, v;  // v: rows that are copied (append only)
+  RopeRows kinds[3];  // Q and K, which are rotated, and (append only) V, which is copied
   const int* positions;
   long pos_row;
   const double* freqs;
@@ -116,21 +115,6 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a,
   // the columns of the thread's two vectors
   const int c0 = turns ? 8 * g : a.rot + 8 * (g - a.rot / 16);
   const int c1 = c0 + (turns ? half : (a.d - a.rot) / 2);
-  const int nq = a.q.heads, nk = nq + a.k.heads, total = nk + a.v.heads;
-  uint4 x[kRopeRows], y[kRopeRows];
-  auto fetch = [&](int r0) {
-#pragma unroll
-    for (int u = 0; u < kRopeRows; ++u) {
-      const int r = r0 + u * rlanes;
-      if (r < total) {
-        const RopeRows& rows = r < nq ? a.q : r < nk ? a.k : a.v;
-        const int h = r < nq ? r : r < nk ? r - nq : r - nk;
-        const uint16_t* src = rows.src + b * rows.ss.sb + h * rows.ss.sh + n * rows.ss.sn;
-        x[u] = *reinterpret_cast<const uint4*>(src + c0);
-        y[u] = *reinterpret_cast<const uint4*>(src + c1);
-      }
-    }
-  };
   if constexpr (PAGED) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = warp; i < nt; i += kRopeThreads / 32) {
@@ -189,23 +173,37 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeArgs a,
         sn[4 + i] = s[second + i];
       }
     }
-    // rows of K and V whose page is not valid are not written
-    const int last = PAGED && s_page[ti] < 0 ? nq : total;
-    for (int r0 = rl; r0 < last; r0 += kRopeRows * rlanes) {
-      fetch(r0);
+#pragma unroll 1
+    for (int kind = 0; kind < (PAGED ? 3 : 2); ++kind) {
+      const RopeRows& rows = a.kinds[kind];
+      // append: K and V rows go to row s_row of page s_page (sb: the page stride), if it is one
+      const bool paged = PAGED && kind > 0;
+      if (paged && s_page[ti] < 0) break;
+      const uint16_t* src = rows.src + b * rows.ss.sb + n * rows.ss.sn;
+      uint16_t* dst = rows.dst + (paged ? s_page[ti] : b) * rows.sd.sb +
+                      (paged ? s_row[ti] : n) * rows.sd.sn;
+      const bool rotate = turns && kind < 2;
+#pragma unroll 1
+      for (int h0 = rl; h0 < rows.heads; h0 += kRopeRows * rlanes) {
+        uint4 x[kRopeRows], y[kRopeRows];
 #pragma unroll
-      for (int u = 0; u < kRopeRows; ++u) {
-        const int r = r0 + u * rlanes;
-        if (r < last) {
-          if (turns && r < nk) rotate16<BF16>(x[u], y[u], cs, sn, interleaved);
-          const RopeRows& rows = r < nq ? a.q : r < nk ? a.k : a.v;
-          const int h = r < nq ? r : r < nk ? r - nq : r - nk;
-          // append: K and V rows go to row s_row of page s_page (sb: the page stride)
-          const bool paged = PAGED && r >= nq;
-          uint16_t* dst = rows.dst + (paged ? s_page[ti] : b) * rows.sd.sb + h * rows.sd.sh +
-                          (paged ? s_row[ti] : n) * rows.sd.sn;
-          *reinterpret_cast<uint4*>(dst + c0) = x[u];
-          *reinterpret_cast<uint4*>(dst + c1) = y[u];
+        for (int u = 0; u < kRopeRows; ++u) {
+          const int h = h0 + u * rlanes;
+          if (h < rows.heads) {
+            const uint16_t* at = src + h * rows.ss.sh;
+            x[u] = *reinterpret_cast<const uint4*>(at + c0);
+            y[u] = *reinterpret_cast<const uint4*>(at + c1);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeRows; ++u) {
+          const int h = h0 + u * rlanes;
+          if (h < rows.heads) {
+            if (rotate) rotate16<BF16>(x[u], y[u], cs, sn, interleaved);
+            uint16_t* at = dst + h * rows.sd.sh;
+            *reinterpret_cast<uint4*>(at + c0) = x[u];
+            *reinterpret_cast<uint4*>(at + c1) = y[u];
+          }
         }
       }
     }
