@@ -282,10 +282,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         more = __all_sync(0xffffffffu, ring.get(&w, &ok, abort_flag));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (more) {
-          ring.read(lane == 0);
-          if (w.j0 >= w.j1) continue;
-        }
+        if (more) ring.read(lane == 0);
+        // An item without tiles, like the end, only ends the item before: the softmax warps
+        // wait for that one's last products before they read on.
+        const bool work = __all_sync(0xffffffffu, more && w.j0 < w.j1);
         ChunkTiles t(w, tpt, wl, wr);
         t.one = __all_sync(0xffffffffu, t.one);
         t.first = __shfl_sync(0xffffffffu, t.first, 0);
@@ -295,10 +295,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           t.lo[g] = __shfl_sync(0xffffffffu, t.lo[g], 0);
           t.hi[g] = __shfl_sync(0xffffffffu, t.hi[g], 0);
         }
-        // after the last item, one turn for the products that are owed
-        const int last = more ? t.last : t.first + 1;
+        // without tiles, one turn for the products that are owed
+        const int last = work ? t.last : t.first + 1;
         for (int tile = t.first; ok && tile < last; ++tile) {
-          if (more && !t.one && tile > t.first && owed[0] && owed[1] && owed[2] && owed[3] &&
+          if (work && !t.one && tile > t.first && owed[0] && owed[1] && owed[2] && owed[3] &&
               t.in(0, tile) && t.in(1, tile)) {
             const uint32_t v = vi - 1;  // owed by all four
             const uint32_t vs = v % kChunkVStages;
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 others = others || (k != i && owed[k] != 0 && owed[k] >> 2 == v);
               if (!others) warp_mma_commit(bar(Lay::bVEmpty + vs));
             }
-            if (more && t.in(g, tile)) {
+            if (work && t.in(g, tile)) {
               if (tile == t.first)
                 ok = warp_wait(bar(Lay::bQFull), static_cast<uint32_t>(item) & 1, abort_flag);
               if (ok && !k_waited) ok = warp_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) owed[k] = k == i ? next : owed[k];
           }
-          if (!ok || !more) break;
+          if (!ok || !work) break;
           warp_mma_commit(bar(Lay::bKEmpty + ks));
           ++vi;
           if (++ks == kChunkKStages) {
@@ -404,9 +404,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             kphase ^= 1;
           }
         }
-        if (!ok || !more) break;
-        warp_mma_commit(bar(Lay::bQEmpty));
-        ++item;
+        if (!ok) break;
+        if (work) {
+          warp_mma_commit(bar(Lay::bQEmpty));
+          ++item;
+        }
       }
     }
   } else if (warp < 8) {

@@ -261,11 +261,17 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
         return true;
       };
       int it = 0, item = 0;
-      bool last_accumulates = false;
+      bool owed = false, last_accumulates = false;  // the product of tile it - 1
       while (ok && __all_sync(0xffffffffu, ring.get(&w, &ok, abort_flag))) {
         ring.read(lane == 0);
         const int j0 = __shfl_sync(0xffffffffu, w.j0, 0), j1 = __shfl_sync(0xffffffffu, w.j1, 0);
-        if (j0 >= j1) continue;
+        if (j0 >= j1) {
+          // an item without tiles: the softmax warps wait for the item before's last product
+          // before they read on
+          if (owed) ok = product(it - 1, last_accumulates);
+          owed = false;
+          continue;
+        }
         const int qb = item & 1;
         ok = warp_wait(bar(Lay::bQFull + qb), static_cast<uint32_t>(item >> 1) & 1, abort_flag);
         const SmemDesc dq = smem_desc(sbase + Lay::kQ + qb * Lay::kQBytes, 16, 1024);
@@ -282,12 +288,13 @@ __global__ void __launch_bounds__(StepLayout<D, NQ>::kThreads, 1)
                         (k >> 2) * Lay::kQChunk + (k & 3) * 32, id_s, k > 0 ? 1u : 0u);
           warp_mma_commit(bar(Lay::bSFull + (it & 1)));
           if (j == j1 - 1) warp_mma_commit(bar(Lay::bQEmpty + qb));
-          if (it > 0) ok = product(it - 1, last_accumulates);
+          if (owed) ok = product(it - 1, last_accumulates);
+          owed = true;
           last_accumulates = j > j0;
         }
         ++item;
       }
-      if (ok && it > 0) product(it - 1, last_accumulates);
+      if (ok && owed) product(it - 1, last_accumulates);
     }
   } else {
     // ----------------------------------------------------------------- softmax

@@ -83,6 +83,21 @@ def test_attention(index, dtype):
     attend(batch, window, d)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 40, 140])
+def test_runs_of_sequences_without_keys(n, d):
+    """Behind each sequence with keys come many items without any, more than a CTA holds in
+    its ring: those must not wait for the products that the item before still owes."""
+    import torch
+    for lengths in ([(n, 300 + n)] + [(n, 0)] * 9) * 8, [(n, 900)] + [(n, 0)] * 60, \
+                   ([(n, 0)] * 5 + [(n, n)] + [(0, 9)] * 3) * 10:
+        batch = make_batch(lengths, 16, 8, d, 32, torch.bfloat16, seed=n)
+        attend(batch, CAUSAL, d)
+        # rows beyond the keys of a sequence see none either
+        batch = make_batch([(n, k // 9) for n, k in lengths], 8, 8, d, 32, torch.float16, seed=d)
+        attend(batch, (0, 0), d)
+
+
 def test_attention_is_the_same_every_time():
     import torch
     batch = make_batch([(70, 5000), (1, 3000), (300, 300)], 8, 2, 128, 16, torch.bfloat16, seed=3)
