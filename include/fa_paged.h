@@ -20,8 +20,10 @@
  * Masks are fa.h's: with off = seq_k[b] - n, query i of a sequence sees key j iff
  * i + off - window_left <= j <= i + off + window_right (negative edge: unbounded);
  * (-1, 0) is causal. Query head h reads key head h / (Hq / heads). A row that sees no key
- * gets O = 0 and L = -inf. V rows that no query of the attention tile at hand sees are
- * never multiplied, whatever they hold; keys that some of them see must be finite.
+ * gets O = 0 and L = -inf. V rows of keys that no query of the attention tile at hand sees
+ * are never multiplied, whatever they hold, nor are pages that only such keys lie in read.
+ * V rows that some of a tile's queries see must be finite (a weight of 0 for the others
+ * does not take a NaN or an infinity away); a NaN score makes its own row's O and L NaN.
  *
  * Lengths, tables and positions are read on the device, so a captured graph follows what
  * they hold when it runs. What the host cannot check is checked there: a sequence whose
@@ -33,8 +35,18 @@
  * Pointers are device pointers of the current device, 16-byte aligned (4 for the 32-bit
  * integer arrays, 8 for freqs); strides are in elements, the last dimension is dense, and
  * the other strides are multiples of 8 elements. Every call only enqueues work on
- * `stream`. The caller owns every buffer; two calls that may run at the same time need
- * workspaces of their own.
+ * `stream`, with launches that overlap the end of the kernel before them; none reads or
+ * writes memory before that kernel has ended. The caller owns every buffer; two calls that
+ * may run at the same time need workspaces of their own. Outputs must not overlap inputs
+ * except where a call says so.
+ *
+ * Errors are fa.h's codes, returned before anything is enqueued: FA_ERR_INVALID for null or
+ * misaligned pointers, negative sizes, strides that are negative or no multiple of 8, bad
+ * scales, magnitudes or rotation sizes, a workspace that is too small; FA_ERR_UNSUPPORTED
+ * for dtypes, head dims, page sizes and group sizes other than named below, more than 8192
+ * sequences, 1024 key heads or 2^28 packed rows or keys per sequence, a stride of 0 over
+ * more than one row in an attention, or a batch of 2^31 and more (item, key tile) pairs by
+ * its bounds (tokens, batch, table_width); FA_ERR_CUDA when CUDA refuses a launch.
  */
 #ifndef FA_PAGED_H_
 #define FA_PAGED_H_
@@ -121,10 +133,13 @@ int fa_paged_append(const fa_paged_append_args *args, void *stream);
  * Exact attention of the packed queries q [tokens][heads_q][d] (strides h and n) over the
  * cache: out [tokens][heads_q][d] and lse [heads_q][tokens] (fp32, natural log). heads_q is
  * a multiple of cache.heads, heads_q / cache.heads <= 128. max_q bounds the new tokens of
- * any sequence (one with more is left out, as above); it picks the kernel. Work is shared
- * out evenly over the SMs by key tiles, so a sequence's keys may be split between CTAs; the
- * parts are joined by their log-sum-exps in a fixed order, and results are the same on
- * every call. The workspace is 256-byte aligned; its contents do not matter.
+ * any sequence (one with more is left out, as above); it picks the kernel: up to 16 rows
+ * (tokens x query heads of a key head; 32 at d = 128) are a step, more are a chunk. Work is
+ * shared out evenly over the SMs by key tiles, so a sequence's keys may be split between
+ * CTAs; the parts are joined by their log-sum-exps in a fixed order. Results are the same
+ * bits on every call with the same lengths (the split, and so the rounding, of a sequence
+ * depends on the lengths of the others). The workspace is 256-byte aligned; its contents do
+ * not matter. Two launches.
  */
 typedef struct {
     fa_paged_cache cache;
