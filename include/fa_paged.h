@@ -138,8 +138,10 @@ int fa_paged_append(const fa_paged_append_args *args, void *stream);
  * shared out evenly over the SMs by key tiles, so a sequence's keys may be split between
  * CTAs; the parts are joined by their log-sum-exps in a fixed order. Results are the same
  * bits on every call with the same lengths (the split, and so the rounding, of a sequence
- * depends on the lengths of the others). The workspace is 256-byte aligned; its contents do
- * not matter. Two launches.
+ * depends on the lengths of the others). The weights are rounded to the 16-bit type for
+ * their product with V, relative to about the largest so far: in fp16 those below 2^-14 of
+ * it lose digits and those below 2^-25 vanish. The workspace is 256-byte aligned; its
+ * contents do not matter. Two launches.
  */
 typedef struct {
     fa_paged_cache cache;

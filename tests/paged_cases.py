@@ -14,6 +14,9 @@ Error bounds (u = eps / 2 of the 16-bit type, the relative rounding of one value
   e = A d 2^-23 with A = scale * max_j sum_t |q_t k_jt|, which moves w by a factor within
   1 +- 2 e, O by 4 e W and L by e; sums of up to 2^17 weights in fp32 lanes and their
   logarithm add 2e-6 (1 + |L|).
+  Below 2^-14 an fp16 weight is off by up to 2^-25 instead. The key that set a row's last
+  reference has weight 1, so sum w >= 1 in every part, and this moves O by at most
+  2^-25 (|v| + |O|) per visible key, numerator and denominator.
 """
 
 from __future__ import annotations
@@ -121,6 +124,10 @@ def reference(batch, scale, window):
             else torch.zeros_like(L)
         e = a * d * 2.0 ** -23
         bound = (2 * u / (1 - u) + 4 * e.T[..., None]) * W + u * o.abs() + 2.0 ** -25
+        if batch.q.dtype == torch.float16:
+            seen = (~hidden).double()
+            bound = bound + 2.0 ** -25 * (torch.einsum("ij,jhd->ihd", seen, vv.abs())
+                                          + seen.sum(-1)[:, None, None] * o.abs())
         out.append((o, L, bound, e + 2e-6 * (1 + L.abs().nan_to_num(posinf=0.0))))
     return out
 

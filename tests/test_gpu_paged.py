@@ -312,6 +312,23 @@ def test_chunks_then_steps_equal_the_whole():
     assert (torch.cat(got_l, 1) - rl[0]).abs().max() <= 2e-3
 
 
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("n", [1, 5, 300])
+def test_pages_before_the_window_may_be_gone(n, page):
+    """Pages whose keys all lie before every new token's window are not looked up: their
+    table entries may point nowhere, and the pages may hold other sequences' keys."""
+    import torch
+    left = 333
+    batch = make_batch([(n, 3000), (n, 1111), (n, n + 1)], 8, 2, 128, page, torch.bfloat16,
+                       seed=n)
+    want = attend(batch, (left, 0), 128)
+    for b, (_, k) in enumerate(batch.lengths):
+        gone = max(0, k - n - left) // page
+        batch.page_table[b, :gone] = -1
+    got = attend(batch, (left, 0), 128)  # its status is FA_OK
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_lengths_that_do_not_fit(n):
     """A sequence with more new tokens than max_q, and rows that cu_q gives to nobody."""
