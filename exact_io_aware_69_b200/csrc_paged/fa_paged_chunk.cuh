@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           tc_fence_after();
           const float2 other = join[r];
           const float top = fmaxf(L2, other.x);
-          if (top != -INFINITY) {
+          if (L2 != -INFINITY || other.x != -INFINITY) {  // a NaN stays one
             const float f = ex2_approx(L2 - top), fo = ex2_approx(other.x - top);
             const float inv = 1.f / (f + fo);
             inv_l *= f * inv;

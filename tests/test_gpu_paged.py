@@ -390,6 +390,23 @@ def test_nan_reaches_its_rows_only(n):
         batch.k_pages[page, at % 64, 0] = old
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_in_rows_of_one_key_tile(d):
+    """Rows of a single query tile, whose key tiles are dealt out in turn, that see keys of
+    one tile only, the second of three: a NaN query there is NaN, its neighbours are not."""
+    import torch
+    batch = make_batch([(100, 400)], 1, 1, d, 64, torch.bfloat16, seed=8)
+    for row in (10, 50, 90):  # keys 260 .. 310, 300 .. 350 (one tile), 340 .. 390 (two)
+        q = batch.q.clone()
+        q[row, 0, 5] = float("nan")
+        o, L = fa.paged_attention(q, *batch.cache, max_q=100, window=(50, 0))
+        assert fa.device_status() == fa.FA_OK
+        bad = torch.zeros(100, 1, dtype=torch.bool, device="cuda")
+        bad[row] = True
+        assert torch.equal(o.isnan().all(-1), bad) and torch.equal(o.isnan().any(-1), bad)
+        assert torch.equal(L.isnan().T, bad)
+
+
 def test_a_pool_past_32_bit_offsets():
     """Pages whose elements lie beyond 2^32: written and read in place."""
     import torch
