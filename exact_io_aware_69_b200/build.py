@@ -85,7 +85,7 @@ def parse_ptxas_report(text: str) -> dict:
 # to exactly this many registers per thread at launch, so the compiled kernel must use
 # exactly that many (the library also refuses to launch otherwise).
 FIXED_REGISTERS = {"fa_bwd_main_kernel": 128, "fa_fwd_pp_kernel": 168,
-                   "fa_paged_chunk_kernel": 168}
+                   "fa_paged_chunk_kernelILi64E": 96, "fa_paged_chunk_kernelILi128E": 168}
 
 
 def check_resources(report: dict) -> None:

@@ -279,12 +279,12 @@ int launch_chunk(const AttentionArgs& a) {
   static_assert(Lay::kSmem <= kMaxDynSmem, "shared memory");
   auto kern = fa::fa_paged_chunk_kernel<D, BF16>;
   // The kernel moves registers between warpgroups (setmaxnreg); its split adds up to
-  // exactly 168 registers per thread at launch (the build fails otherwise too).
+  // exactly this many registers per thread at launch (the build fails otherwise too).
   static std::atomic<bool> counted{false};
   if (!counted.load(std::memory_order_relaxed)) {
     cudaFuncAttributes attr;
     if (cudaFuncGetAttributes(&attr, kern) != cudaSuccess) return FA_ERR_CUDA;
-    if (attr.numRegs != fa::kChunkLaunchRegs) return FA_ERR_UNSUPPORTED;
+    if (attr.numRegs != fa::ChunkRoles<D>::kLaunchRegs) return FA_ERR_UNSUPPORTED;
     counted.store(true, std::memory_order_relaxed);
   }
   if (!allow_smem(kern, Lay::kSmem)) return FA_ERR_CUDA;
@@ -298,7 +298,7 @@ int launch_chunk(const AttentionArgs& a) {
                  {a.xo.h, a.xo.n, a.xo.h * a.group}, a.group, out_tokens) ||
       !make_part_tmap(&part, a.opart(), D, 2 * kGrid * a.ws.rows))
     return FA_ERR_CUDA;
-  const int st = launch(kern, dim3(kGrid), fa::kChunkThreads, Lay::kSmem, a.stream, q, k, v,
+  const int st = launch(kern, dim3(kGrid), fa::ChunkRoles<D>::kThreads, Lay::kSmem, a.stream, q, k, v,
                         o, part, view_of(*a.c), static_cast<uint16_t*>(a.O), strides(a.xo), a.L,
                         a.lpart(), a.parts(), a.group, a.max_q, a.wl, a.wr, kLeastCost,
                         a.scale * kLog2e);

@@ -12,33 +12,41 @@
 // with the same number of key tiles, whatever the mix of long chunks and single tokens; a
 // chunk's heavy last rows, or a long context behind a short chunk, cannot leave SMs idle.
 //
-// Warp roles (384 threads; at launch every thread may hold 168 registers, then warpgroup 2
-// hands registers to warpgroups 0 and 1):
-//   warps 0-3, 4-7  softmax of query tile 0 and 1: thread r owns row r (TMEM lane r), so its
-//                   maximum needs no exchange. It takes a tile's keys in two halves of 64.
-//   warp 8          K producer: the item's two Q tiles, then K tiles into 2 stages.
-//   warp 10         V producer, 2 stages. Both walk the page table by themselves, a window
+// Warp roles (at launch every thread holds the same number of registers, then the last
+// warpgroup hands some to the others; warps counted from it):
+//   softmax         thread r of a warpgroup owns row r of its query tile (TMEM lane r), so its
+//                   maximum needs no exchange. A tile's keys go in two halves of 64. At d =
+//                   128 a warpgroup per query tile takes them in turn (384 threads), at d =
+//                   64 there is one for each half (640 threads).
+//   warp 0          K producer: the item's two Q tiles, then K tiles into 2 stages.
+//   warp 2          V producer, 2 stages. Both walk the page table by themselves, a window
 //                   of pages ahead, one box per page and 64 columns.
-//   warp 11         scheduler: the CTA's items.
-//   warp 9          MMA issuer. With S_g,h the scores of query tile g and half h of the tile
+//   warp 3          scheduler: the CTA's items.
+//   warp 1          MMA issuer. With S_g,h the scores of query tile g and half h of the tile
 //                   and PV_g,h their weights' product, it issues for each tile
 //                     PV_0,0 S_0,0  PV_1,0 S_1,0  PV_0,1 S_0,1  PV_1,1 S_1,1
 //                   each PV that of the tile before. The order runs on across items: the
 //                   next item's first scores are computed while this one's outputs leave.
 //
-// TMEM (512 columns at d = 128): 64 columns of scores per (g, h) at 128 g + 64 h, whose first
-// 32 the weights P take over; O of g at 256 + d g. Because a half's scores wait only for
-// the product of the half two before, they are there when the softmax has finished the half
-// in between: it never waits for the tensor core's round trip, which with whole-tile
-// buffers was half of its time. Products of a g run in order; O_g may be rescaled once the
-// product before has landed (a barrier, waited for only when a row's reference moves past
-// 2^8, and at the item's end).
+// TMEM (512 columns): 64 columns of scores per (g, h) at 128 g + 64 h, whose first 32 the
+// weights P take over; behind them O of g, at d = 64 of (g, h). Because a half's scores wait
+// only for the product of the half two before, they are there when the softmax has finished
+// the half in between: it never waits for the tensor core's round trip, which with
+// whole-tile buffers was half of its time. Products into an O run in order; it may be
+// rescaled once the product before has landed (a barrier, waited for only when a row's
+// reference moves past 2^8, and at the item's end).
+//
+// The two halves apart at d = 64: the exponentials bound that size (a tile's products take
+// half as long as at d = 128, its softmax as long), and two softmax warps per scheduler left
+// their unit idle 39 % of the time; with four, 2048 tokens over 16k keys (32 heads) take 306
+// us for 365, 827 TFLOP/s. Each has a reference, a sum and an O of its own, joined at an
+// item's end. At d = 128 tensor memory has no room for four O.
 //
 // An item with one query tile (a single token among chunks, a short draft, a chunk's last
-// tokens) would leave one warpgroup idle and the tensor core waiting for the other. There
-// the two take the key tiles in turn, both with query tile 0, and warpgroup 0 joins the two
-// partial outputs out of tensor memory by their log-sum-exps. Warps none of whose rows is a
-// real query skip the softmax.
+// tokens) would leave one half of the warps idle and the tensor core waiting for the other.
+// There the two groups take the key tiles in turn, both with query tile 0, and the first
+// warpgroup joins the partial outputs out of tensor memory by their references and sums.
+// Warps none of whose rows is a real query skip the softmax.
 //
 // Scores are in base 2. One row sum, of the unrounded weights, gives L and normalises O. (The
 // product multiplies weights rounded to 16 bits. A second sum, of those, would make O an
@@ -53,14 +61,21 @@
 
 namespace fa {
 
-constexpr int kChunkThreads = 384;
-constexpr int kChunkKWarp = 8, kChunkMmaWarp = 9, kChunkVWarp = 10, kChunkScheduler = 11;
-// 168 registers per thread at launch (the most 384 threads can have), then per
-// sub-partition 2 x 216 (softmax) + 72 (producers, MMA) = 3 x 168.
-constexpr int kChunkLaunchRegs = 168;
-constexpr int kChunkSoftmaxRegs = 216;
-constexpr int kChunkSmallRegs = 72;
-static_assert(2 * kChunkSoftmaxRegs + kChunkSmallRegs == 3 * kChunkLaunchRegs, "register split");
+// Warps by head size.
+template <int D>
+struct ChunkRoles {
+  static constexpr int kHalves = D == 64 ? 2 : 1;  // softmax warpgroups per query tile
+  static constexpr int kSoftmaxWarps = 8 * kHalves;
+  static constexpr int kK = kSoftmaxWarps, kMma = kK + 1, kV = kK + 2, kScheduler = kK + 3;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+  // Registers per thread at launch (the most that many threads can have), then those of
+  // the softmax warpgroups and of the last one; the sums must be equal.
+  static constexpr int kLaunchRegs = D == 64 ? 96 : 168;
+  static constexpr int kSoftmaxRegs = D == 64 ? 104 : 216;
+  static constexpr int kSmallRegs = D == 64 ? 64 : 72;
+  static_assert(2 * kHalves * kSoftmaxRegs + kSmallRegs == (2 * kHalves + 1) * kLaunchRegs,
+                "register split");
+};
 constexpr float kChunkRescaleSlack = 8.0f;
 constexpr int kChunkRows = 256;  // rows of an item
 constexpr int kChunkKStages = 2;
@@ -74,14 +89,17 @@ struct ChunkLayout {
   static constexpr uint32_t kK = kQ + 2 * kTileBytes;
   static constexpr uint32_t kV = kK + kChunkKStages * kTileBytes;
   static constexpr uint32_t kOut = kV + kChunkVStages * kTileBytes;  // 4 KB per softmax warp
-  static constexpr uint32_t kItems = kOut + 8 * 4096;
-  static constexpr uint32_t kJoin = kItems + kItemSlots * sizeof(Item);  // [row] of group 1
-  static constexpr uint32_t kBar = kJoin + 128 * 8;
+  static constexpr uint32_t kItems = kOut + 8 * 4096;  // (of the warps that store)
+  // [warpgroup - 1][row] (reference, sum) of the softmax warpgroups that do not store
+  static constexpr uint32_t kJoin = kItems + kItemSlots * sizeof(Item);
+  static constexpr uint32_t kBar = kJoin + (2 * ChunkRoles<D>::kHalves - 1) * 128 * 8;
   static constexpr int bQFull = 0, bQEmpty = 1, bKFull = 2, bKEmpty = bKFull + kChunkKStages,
                        bVFull = bKEmpty + kChunkKStages, bVEmpty = bVFull + kChunkVStages,
                        bSFull = bVEmpty + kChunkVStages,  // + 2 g + h, as the next two
                        bPFull = bSFull + 4, bDone = bPFull + 4, bJoin = bDone + 4,
-                       bJoined = bJoin + 1, bItems = bJoined + 1,
+                       bJoined = bJoin + 1,
+                       bPair = bJoined + 1, bPaired = bPair + 2,  // + group
+                       bItems = bPaired + 2,
                        kNumBars = bItems + 2 * kItemSlots;
   static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
   static constexpr uint32_t kAbort = kTmemSlot + 8;
@@ -89,7 +107,7 @@ struct ChunkLayout {
   // at least 120 KB, so that one CTA and its 512 TMEM columns sit on each SM
   static constexpr uint32_t kSmem = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
   static constexpr uint32_t tS = 0;    // + 128 * warpgroup + 64 * half
-  static constexpr uint32_t tO = 256;  // + D * warpgroup
+  static constexpr uint32_t tO = 256;  // + D * group, or 64 * (2 * group + half) at d = 64
 };
 
 // The key tiles that each warpgroup of an item takes part in, within the CTA's part.
@@ -122,7 +140,7 @@ struct ChunkTiles {
 };
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kChunkThreads, 1)
+__global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
     fa_paged_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV,
@@ -134,11 +152,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                           int least,
                           float scale_log2) {
   using Lay = ChunkLayout<D>;
+  using Roles = ChunkRoles<D>;
+  constexpr bool kOwn = Roles::kHalves == 2;  // a half of the keys has an O of its own
   // Of every 16 exponential pairs, kPolyPairs go to the FMA pipe: 2048 tokens over 16k keys
-  // (32 heads) take 447 / 444 / 431 / 428 us at d = 128 with 0 / 1 / 2 / 4 of them, 369 / 357 /
-  // 376 at d = 64 with 0 / 2 / 4. (Masked scores may take the polynomial: its 2^-125 for them
+  // (32 heads) take 447 / 444 / 431 / 428 us at d = 128 with 0 / 1 / 2 / 4 of them, 310 / 306 /
+  // 331 at d = 64 with 2 / 4 / 8. (Masked scores may take the polynomial: its 2^-125 for them
   // vanishes next to the row's own weights, and in a row without any nothing is read.)
-  constexpr int kPolyPairs = D == 64 ? 2 : 4;
+  constexpr int kPolyPairs = 4;
   constexpr int kPolyStride = 16 / kPolyPairs;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
@@ -171,24 +191,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(bar(Lay::bPFull + i), 128);
       mbar_init(bar(Lay::bDone + i), 1);
     }
-    mbar_init(bar(Lay::bJoin), 128);
+    mbar_init(bar(Lay::bJoin), 128 * (2 * Roles::kHalves - 1));
     mbar_init(bar(Lay::bJoined), 128);
-    item_ring_init(bar(Lay::bItems), 11);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(bar(Lay::bPair + g), 128);
+      mbar_init(bar(Lay::bPaired + g), 128);
+    }
+    item_ring_init(bar(Lay::bItems), Roles::kSoftmaxWarps + 3);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kChunkMmaWarp) {
+  if (warp == Roles::kMma) {
     tmem_alloc(sbase + Lay::kTmemSlot, 512);
     tmem_relinquish();
   }
   // rows of the Q tiles that no box fills stay zero
   if (tpt * group < kKeyTile)
-    for (uint32_t i = threadIdx.x; i < 2 * Lay::kTileBytes / 16; i += kChunkThreads)
+    for (uint32_t i = threadIdx.x; i < 2 * Lay::kTileBytes / 16; i += Roles::kThreads)
       *reinterpret_cast<uint4*>(smem + Lay::kQ + i * 16) = make_uint4(0u, 0u, 0u, 0u);
   fence_async_smem();
   dependency_wait();
   Scheduler<false> schedule(c, tpi, max_q, wl, wr);
-  if (warp == kChunkScheduler) schedule.locate(least);
+  if (warp == Roles::kScheduler) schedule.locate(least);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -197,12 +221,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   Item w;
   bool ok = true;
 
-  if (warp >= 8) setmaxnreg_dec<kChunkSmallRegs>();  // every warp of warpgroup 2
-  if (warp == kChunkScheduler) {
+  if (warp >= Roles::kSoftmaxWarps) setmaxnreg_dec<Roles::kSmallRegs>();  // the last warpgroup
+  if (warp == Roles::kScheduler) {
     schedule.run(ring, abort_flag, parts);
-  } else if (warp == kChunkKWarp || warp == kChunkVWarp) {
+  } else if (warp == Roles::kK || warp == Roles::kV) {
     // ---------------------------------------------------------------- producers
-    const bool is_k = warp == kChunkKWarp;
+    const bool is_k = warp == Roles::kK;
     const CUtensorMap* map = is_k ? &tmK : &tmV;
     const int stages = is_k ? kChunkKStages : kChunkVStages;
     const uint32_t tiles = sbase + (is_k ? Lay::kK : Lay::kV);
@@ -260,7 +284,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
     if (win.bad) atomicExch(&g_fa_status, kStatusInvalid);
-  } else if (warp == kChunkMmaWarp) {
+  } else if (warp == Roles::kMma) {
     // -------------------------------------------------------------- MMA issuer
     {
       constexpr uint32_t idesc_s = idesc_f16_f32(kKeyTile, 64, BF16, false, false);
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
             for (int turn = 0; turn < 4; ++turn) {
               const int h = turn >> 1, g = turn & 1, i = 2 * g + h;
-              const uint32_t d_s = tmem + Lay::tS + g * 128 + h * 64, d_o = tmem + Lay::tO + g * D;
+              const uint32_t d_s = tmem + Lay::tS + g * 128 + h * 64, d_o = tmem + Lay::tO + (kOwn ? i : g) * D;
               ok = warp_wait(bar(Lay::bPFull + i), pphase >> i & 1u, abort_flag) &&
                    (turn > 0 || (warp_wait(bar(Lay::bVFull + vs), (v / kChunkVStages) & 1,
                                            abort_flag) &&
@@ -360,7 +384,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               tc_fence_after();
               const SmemDesc dv = smem_desc(sbase + Lay::kV + vs * Lay::kTileBytes + h * 8192,
                                               Lay::kChunkBytes, 1024);
-              const uint32_t d_o = tmem + Lay::tO + g * D;
+              const uint32_t d_o = tmem + Lay::tO + (kOwn ? i : g) * D;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 warp_mma_ts(d_o, d_s + k * 8, dv, k * 2048, idesc_o,
@@ -391,7 +415,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 warp_mma_ss(d_s, dq, koff, dk, koff, idesc_s, k > 0 ? 1u : 0u);
               }
               warp_mma_commit(bar(Lay::bSFull + i));
-              next = (h == 0 && tile == (g ? t.lo[1] : t.lo[0]) ? 1u : 2u) + 4u * vi;
+              next = ((kOwn || h == 0) && tile == (g ? t.lo[1] : t.lo[0]) ? 1u : 2u) + 4u * vi;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) owed[k] = k == i ? next : owed[k];
@@ -411,19 +435,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < Roles::kSoftmaxWarps) {
     // ----------------------------------------------------------------- softmax
-    setmaxnreg_inc<kChunkSoftmaxRegs>();
-    const int g = warp >> 2;
+    setmaxnreg_inc<Roles::kSoftmaxRegs>();
+    const int g = warp / (4 * Roles::kHalves);
+    const int half = kOwn ? warp >> 2 & 1 : 0;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row of the query tile = TMEM lane
     const int tr = r * by_group >> 16;  // its token in the tile (tpt or more: a row of zeros)
     const int head_in = r - tr * group;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t o_cols = Lay::tO + g * D;
+    const uint32_t o_cols = Lay::tO + (kOwn ? 2 * g + half : g) * D;
     const uint64_t c2 = f2_pack(scale_log2, scale_log2);
     uint32_t used = 0;  // tiles of this group before: phases of its S, P and product barriers
-    uint32_t jphase = 0;
+    uint32_t jphase = 0, pair_phase = 0;
     int vi = 0;  // V tiles of the CTA before this item
     while (ok) {
       if (!__all_sync(0xffffffffu, ring.get(&w, &ok, abort_flag))) break;
@@ -451,7 +476,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       float l = 0.f;        // row sum of p
       for (int tile = lo; ok && tile < hi; tile += step, ++used) {
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
+        for (int h = half; h < (kOwn ? half + 1 : 2); ++h) {
           const uint32_t bars = 2 * g + h;
           ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bSFull + bars), used & 1, abort_flag));
           if (!ok) break;
@@ -508,23 +533,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             tmem_wait_st();
           }
-          float s[64];
-          {
-            uint32_t sr[64];
-            tmem_ld32(lane_base + s_cols, sr);
-            tmem_ld32(lane_base + s_cols + 32, sr + 32);
-            tmem_wait_ld();
-            reg_fence32(sr);
-            reg_fence32(sr + 32);
-#pragma unroll
-            for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(sr[e]);
-          }
-          // row maximum over four independent chains
+          // row maximum over four independent chains; at d = 64 the upper half of the scores is
+          // read again for its exponentials, so that 32 stay in registers
+          constexpr int kHeld = kOwn ? 32 : 64;
+          float s[kHeld];
           float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 64; i += 8) {
+          for (int part = 64 - kHeld; part >= 0; part -= kHeld) {
+            uint32_t sr[kHeld];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mq[k] = fmax3(mq[k], s[i + 2 * k], s[i + 2 * k + 1]);
+            for (int i = 0; i < kHeld; i += 32) tmem_ld32(lane_base + s_cols + part + i, sr + i);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < kHeld; i += 32) reg_fence32(sr + i);
+#pragma unroll
+            for (int e = 0; e < kHeld; ++e) s[e] = __uint_as_float(sr[e]);
+#pragma unroll
+            for (int i = 0; i < kHeld; i += 8) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mq[k] = fmax3(mq[k], s[i + 2 * k], s[i + 2 * k + 1]);
+            }
           }
           const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
           const float cand = mx * scale_log2;
@@ -538,9 +566,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             uint32_t pk[16];
+            if (kOwn && j == 1) {
+              uint32_t sr[32];
+              tmem_ld32(lane_base + s_cols + 32, sr);
+              tmem_wait_ld();
+              reg_fence32(sr);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(sr[e]);
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int e = j * 32 + 2 * i;
+              const int e = j * (kHeld - 32) + 2 * i;
               float x0, x1;
               f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), c2, nm2), x0, x1);
               float p0, p1;
@@ -560,9 +596,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           l = l * alpha + (a0 + a1);
           // a reference moved, and O holds products: once the last of them has landed (that
           // of the half before; the one before that landed ahead of these scores)
-          if ((tile > lo || h > 0) && __any_sync(0xffffffffu, alpha != 1.f)) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bDone + (bars ^ 1)),
-                                                   (h ? used : used - 1) & 1, abort_flag));
+          if ((tile > lo || (!kOwn && h > 0)) && __any_sync(0xffffffffu, alpha != 1.f)) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bDone + (kOwn ? bars : bars ^ 1)),
+                                                   (!kOwn && h ? used : used - 1) & 1,
+                                                   abort_flag));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -586,41 +623,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const bool some = lo < hi;
       ok = __all_sync(
           0xffffffffu,
-          ok && (!some || (mbar_wait(bar(Lay::bDone + 2 * g), (used - 1) & 1, abort_flag) &&
-                           mbar_wait(bar(Lay::bDone + 2 * g + 1), (used - 1) & 1, abort_flag))));
+          ok && (!some || (mbar_wait(bar(Lay::bDone + 2 * g + half), (used - 1) & 1, abort_flag) &&
+                           (kOwn || mbar_wait(bar(Lay::bDone + 2 * g + 1), (used - 1) & 1,
+                                              abort_flag)))));
       tc_fence_after();
-      // rows that see no key: O = 0, L = -inf (their sums need not be 0: the polynomial's
-      // least value is 2^-125); a NaN among the scores shows in the sum and stays one
-      const bool none = m == -INFINITY && l == l;
-      float L2 = none ? -INFINITY : m + log2f(l);
-      float inv_l = none ? 0.f : 1.f / l;
-      float inv_other = 0.f;
-      float2* join = reinterpret_cast<float2*>(smem + Lay::kJoin);
-      if (one && ok) {  // group 1 hands over
-        if (g == 1) {
-          join[r] = make_float2(L2, inv_l);
-          mbar_arrive(bar(Lay::bJoin));
+      // Warpgroups that share a query tile -- all where it is the item's only one, else, at d =
+      // 64, the two halves of its keys -- join their sums; the first of them stores.
+      const int me = kOwn ? 2 * g + half : g;
+      const int sharing = one ? 2 * Roles::kHalves : Roles::kHalves;
+      const bool stores = me % sharing == 0;
+      float2* sums = reinterpret_cast<float2*>(smem + Lay::kJoin) + r;
+      float top = m;
+      if (sharing > 1 && ok) {
+        const uint32_t told = bar(one ? Lay::bJoin : Lay::bPair + g);
+        if (!stores) {
+          sums[(me - 1) * 128] = make_float2(m, l);
+          mbar_arrive(told);
         } else {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bJoin), jphase, abort_flag));
+          ok = __all_sync(0xffffffffu, mbar_wait(told, one ? jphase : pair_phase, abort_flag));
           tc_fence_after();
-          const float2 other = join[r];
-          const float top = fmaxf(L2, other.x);
-          if (L2 != -INFINITY || other.x != -INFINITY) {  // a NaN stays one
-            const float f = ex2_approx(L2 - top), fo = ex2_approx(other.x - top);
-            const float inv = 1.f / (f + fo);
-            inv_l *= f * inv;
-            inv_other = other.y * fo * inv;
-            L2 = top + log2f(f + fo);
-          }
+#pragma unroll 1
+          for (int i = me + 1; i < me + sharing; ++i) top = fmaxf(top, sums[(i - 1) * 128].x);
         }
       }
+      // Rows that see no key keep the reference -inf, and their sums (which need not be 0: the
+      // polynomial's least value is 2^-125) a factor of 0: O = 0, L = -inf. A NaN among the
+      // scores shows in a sum and stays one.
+      const float top_sub = top == -INFINITY ? 0.f : top;
+      float inv_l = ex2_approx(m - top_sub);
+      if (stores) {
+        l *= inv_l;
+#pragma unroll 1
+        for (int i = me + 1; i < me + sharing; ++i) {
+          const float2 other = sums[(i - 1) * 128];
+          const float f = ex2_approx(other.x - top_sub);
+          l = fmaf(other.y, f, l);
+          sums[(i - 1) * 128].x = f;  // read again by this thread, with that warpgroup's O
+        }
+      }
+      const float L2 = top_sub + log2f(l);
+      const float inv_sum = l == 0.f ? 0.f : 1.f / l;
+      inv_l *= inv_sum;
       // O / l: a thread holds a row, a store wants rows' neighbours side by side, so 128
       // bytes of each row (64 columns, or 32 of a part in fp32) at a time go through the
       // warp's 4 KB of shared memory, 128-byte-swizzled, and leave in one TMA store (of a
       // part's rows, or of whole tokens when 32 rows are that) or, at a sequence's ragged end,
       // as four rows an instruction. (Straight from the rows' threads an item's store took
       // 3000 to 8000 cycles.)
-      if (ok && busy && !(one && g == 1)) {
+      if (ok && busy && stores) {
         const bool whole = w.j0 == 0 && w.j1 == w.keys.count;
         const bool other_some = one && first + 1 < w.keys.first + w.j1;
         const int rows = min(tpt, w.n - tok0) * group;  // of the query tile
@@ -629,7 +679,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int slot_row = (w.j0 > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * kChunkRows +
                              (one ? 0 : g * kKeyTile);
         const bool by_tma = !whole || (32 % group == 0 && row0 + 32 <= rows);
-        const uint32_t stage = sbase + Lay::kOut + warp * 4096;
+        const uint32_t stage = sbase + Lay::kOut + (4 * g + quarter) * 4096;
 #pragma unroll 1
         for (int i = 0; i < D; i += 32) {
           float x[32];
@@ -644,15 +694,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = 0.f;
           }
-          if (other_some) {
-            tmem_ld32(lane_base + Lay::tO + D + i, o);
+#pragma unroll 1
+          for (int k = me + 1; k < me + sharing; ++k) {
+            if (!(one && k >= Roles::kHalves ? other_some : some)) break;
+            const float f = sums[(k - 1) * 128].x * inv_sum;
+            tmem_ld32(lane_base + Lay::tO + k * D + i, o);
             tmem_wait_ld();
             reg_fence32(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o[e]), inv_other, x[e]);
+            for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o[e]), f, x[e]);
           }
-          // the bytes before have left (they did so at once, except by TMA)
-          if (lane == 0 && by_tma && (!whole || (i & 32) == 0)) bulk_wait_read_all();
+          // the bytes before, of this item or the last, have left
+          if (lane == 0 && (!whole || (i & 32) == 0)) bulk_wait_read_all();
           __syncwarp();
           if (whole) {  // half of the row's 128 bytes; they leave after the second half
             const int half = (i >> 5) & 1;
@@ -704,8 +757,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             __syncwarp();
           }
         }
-        // what left by TMA has to be out before the CTA ends, and read before it is reused
-        if (lane == 0 && by_tma) bulk_wait_all();
         if (r < rows) {
           if (whole)
             L[static_cast<long>(w.h * group + head_in) * c.tokens + w.begin + tok0 + tr] =
@@ -715,19 +766,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       tc_fence_before();
-      if (one && ok) {  // O of group 1 has been read
-        if (g == 0)
-          mbar_arrive(bar(Lay::bJoined));
+      if (sharing > 1 && ok) {  // the others' sums and O have been read
+        const uint32_t read = bar(one ? Lay::bJoined : Lay::bPaired + g);
+        if (stores)
+          mbar_arrive(read);
         else
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(Lay::bJoined), jphase, abort_flag));
-        jphase ^= 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(read, one ? jphase : pair_phase, abort_flag));
+        if (one)
+          jphase ^= 1;
+        else
+          pair_phase ^= 1;
       }
     }
+    if (lane == 0) bulk_wait_all();  // what left by TMA is out before the CTA ends
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kChunkMmaWarp) {
+  if (warp == Roles::kMma) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -178,7 +178,7 @@ def test_workspace_size(lib):
 
 # Threads per block of every kernel the library launches.
 BLOCK_THREADS = {"fa_rope_kernel": 128, "fa_paged_step_kernel": 256, "fa_paged_merge_kernel": 256,
-                 "fa_paged_chunk_kernel": 384}
+                 "fa_paged_chunk_kernelILi64E": 640, "fa_paged_chunk_kernelILi128E": 384}
 
 
 def test_every_kernel_fits_the_register_file_at_its_block_size():
