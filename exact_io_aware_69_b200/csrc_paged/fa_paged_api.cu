@@ -252,7 +252,7 @@ bool allow_smem(Kernel kernel, size_t smem) {
                               static_cast<int>(smem)) == cudaSuccess;
 }
 
-// The least cost (in key tiles, kItemCost of them for an item) that is worth a CTA of its
+// The least cost (in key tiles, those for starting an item included) that is worth a CTA of its
 // own: one token over 1000 keys (32 heads over 8) takes 9.2 / 9.5 / 9.9 / 10.7 / 13.3 us
 // with 1 / 2 / 3 / 4 / 8, over 4000 keys 11.2 / 10.7 / 10.8 / 11.2 / 13.6, a prompt of 300
 // tokens 18.2 / 21.5 / 25.4 / 30.3 with 2 / 4 / 6 / 8.
@@ -411,7 +411,7 @@ int fa_paged_attention(const fa_paged_attention_args* args, void* stream) {
   const int tpi = ws.rows == fa::kChunkRows ? 2 * (fa::kKeyTile / group) : max_q;
   const long long items = c.tokens / tpi + c.batch;
   const long long tiles = static_cast<long long>(c.table_width) * c.page_size / fa::kKeyTile + 2;
-  if (items * c.heads > fa::kMaxCost / (tiles + fa::kItemCost)) return FA_ERR_UNSUPPORTED;
+  if (items * c.heads > fa::kMaxCost / (tiles + fa::kChunkItemCost)) return FA_ERR_UNSUPPORTED;
   if (!ok_ptr(r.workspace, 256) || r.workspace_bytes < ws.bytes) return FA_ERR_INVALID;
   const AttentionArgs a{&c,
                         r.q,

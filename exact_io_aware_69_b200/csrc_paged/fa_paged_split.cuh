@@ -2,12 +2,12 @@
 //
 // An item is what one pass over keys serves: up to `tpi` consecutive new tokens of one
 // sequence, all query heads of one key head. Its cost is the key tiles (128 keys) that its
-// rows see, plus kItemCost for starting and finishing it. The items, ordered by (sequence,
+// rows see, plus `start` tiles for starting and finishing it. The items, ordered by (sequence,
 // key head, place in the sequence), lie end to end on a line of cost, and CTA c of C takes
 // the stretch [W c / C, W (c + 1) / C) of it: every CTA gets the same work whatever the
 // lengths, an item that crosses a boundary is computed in parts, and each CTA has at most
 // two parts (its first item's end, its last item's beginning). A boundary within an
-// item's first kItemCost units moves to the item's start, so that no part is empty.
+// item's first `start` units moves to the item's start, so that no part is empty.
 //
 // The split depends only on the lengths, the mask and the grid, so the parts and the order
 // in which they are joined -- and with them every rounding -- are the same on every call.
@@ -23,9 +23,13 @@
 namespace fa {
 
 constexpr int kKeyTile = 128;
-// About two tiles' time: an item's first scores wait for its first keys, and its last
-// product is followed by the sums and the store.
-constexpr int kItemCost = 2;
+// Starting and finishing an item in key tiles' time: its first scores wait for its first
+// keys, and its last product is followed by the sums and the store. 64 single tokens over
+// 300 to 16,384 keys take 160 / 163 / 165 us with 2 / 3 / 4; prompts of 100 to 2000 tokens
+// with and without single tokens 77.7 / 75.6 / 73.4 and 116 / 104 / 108 us (d = 64),
+// 124 / 117 / 119 and 152 / 136 / 137 (d = 128).
+constexpr int kStepItemCost = 2;
+constexpr int kChunkItemCost = 3;
 
 struct KeyRange {
   int lo, hi;        // keys that some row of the item sees (lo > hi: none)
@@ -45,7 +49,7 @@ __host__ __device__ inline KeyRange item_keys(int p, int tpi, int n, int nk, int
   return r;
 }
 __host__ __device__ inline int items_of(int n, int tpi) { return (n + tpi - 1) / tpi; }
-__host__ __device__ inline int item_cost(const KeyRange& r) { return r.count + kItemCost; }
+__host__ __device__ inline int item_cost(const KeyRange& r, int start) { return r.count + start; }
 
 // CTAs of an attention launch: one per SM of a B200. A fixed count keeps the split the
 // same everywhere, and divisions by it are multiplications.
@@ -59,8 +63,8 @@ __host__ __device__ inline unsigned split_start(unsigned W, unsigned c, unsigned
   return x < W ? x : W;
 }
 // The tile at which a boundary `r` units into an item cuts it (0: before the item).
-__host__ __device__ inline int split_tile(unsigned r) {
-  return r <= static_cast<unsigned>(kItemCost) ? 0 : static_cast<int>(r) - kItemCost;
+__host__ __device__ inline int split_tile(unsigned r, int start) {
+  return r <= static_cast<unsigned>(start) ? 0 : static_cast<int>(r) - start;
 }
 
 // An item, or the part of it that falls to a CTA: tiles [first + j0, first + j1).
@@ -158,6 +162,7 @@ __device__ __forceinline__ void item_ring_init(uint32_t bars, int readers) {
 // cold from L2 at about 17 cycles each: few of them matter more than their kind.
 template <bool ONE_ITEM>
 struct Scheduler {
+  static constexpr int kStart = ONE_ITEM ? kStepItemCost : kChunkItemCost;
   const PagedView& c;
   const int tpi, max_q, wl, wr, lane;
   int base;       // lane i holds sequence base + i
@@ -176,7 +181,7 @@ struct Scheduler {
     if (i < c.batch) seq = seq_info(c, i, max_q);
   }
   __device__ __forceinline__ unsigned cost_of(int place, int n, int nk) const {
-    return static_cast<unsigned>(item_cost(item_keys(place, tpi, n, nk, wl, wr)));
+    return static_cast<unsigned>(item_cost(item_keys(place, tpi, n, nk, wl, wr), kStart));
   }
   // Cost per key head of this lane's sequence.
   __device__ __forceinline__ unsigned seq_cost() const {
@@ -279,9 +284,9 @@ struct Scheduler {
         for (; ok && more && p * tpi < it.n; ++p) {
           it.p = p;
           it.keys = item_keys(p, tpi, it.n, it.nk, wl, wr);
-          const unsigned cost = item_cost(it.keys);
-          it.j0 = at < x0 ? split_tile(x0 - at) : 0;
-          it.j1 = at + cost <= x1 ? it.keys.count : split_tile(x1 - at);
+          const unsigned cost = item_cost(it.keys, kStart);
+          it.j0 = at < x0 ? split_tile(x0 - at, kStart) : 0;
+          it.j1 = at + cost <= x1 ? it.keys.count : split_tile(x1 - at, kStart);
           if (it.j1 > it.j0 || (it.keys.count == 0 && at + cost <= x1)) {
             if (it.j1 < it.keys.count) {  // a later CTA goes on with it
               info.goes_on = it.j0 > 0;

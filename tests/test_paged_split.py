@@ -29,13 +29,14 @@ int main() {
       unsigned W, c, least;
       std::scanf("%u %u %u", &W, &c, &least);
       std::printf("%u\n", fa::split_start(W, c, least));
-    } else {  // r
+    } else {  // r start
       unsigned r;
-      std::scanf("%u", &r);
-      std::printf("%d\n", fa::split_tile(r));
+      int start;
+      std::scanf("%u %d", &r, &start);
+      std::printf("%d\n", fa::split_tile(r, start));
     }
   }
-  std::printf("%d %d\n", fa::kSplitGrid, fa::kItemCost);
+  std::printf("%d %d %d\n", fa::kSplitGrid, fa::kStepItemCost, fa::kChunkItemCost);
   return 0;
 }
 '''
@@ -80,7 +81,8 @@ def test_item_keys_against_brute_force(ask):
 @pytest.mark.parametrize("seed", range(30))
 def test_every_tile_in_one_stretch(ask, seed):
     rng = random.Random(seed)
-    grid, overhead = ask([])[-1]
+    grid, *starts_cost = ask([])[-1]
+    overhead = starts_cost[seed % 2]
     counts = [rng.choice([0, 0, 1, 2, 3, rng.randint(1, 40), rng.randint(1, 600)])
               for _ in range(rng.choice([1, 2, 8, 60, 400]))]
     least = rng.choice([1, 2, 4, 9])
@@ -93,7 +95,7 @@ def test_every_tile_in_one_stretch(ask, seed):
     assert all(x >= min(full[:-1] or full) for x in full[:-1]) and \
         (len(full) == 1 or min(full[:-1]) >= least)
     # where a boundary r units into an item cuts it
-    cuts = [t for t, in ask([f"t {r}" for r in range(max(counts) + overhead + 1)])[:-1]]
+    cuts = [t for t, in ask([f"t {r} {overhead}" for r in range(max(counts) + overhead + 1)])[:-1]]
     at, tiles = 0, [[0] * c for c in counts]
     parts = [[] for _ in range(grid)]
     for i, c in enumerate(counts):
