@@ -307,8 +307,9 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (more) ring.read(lane == 0);
-        // An item without tiles, like the end, only ends the item before: the softmax warps
-        // wait for that one's last products before they read on.
+        // First the products that the item before is owed, its softmax warps wait for them
+        // before they read on: a turn without scores. It is all that an item without tiles,
+        // like the end, is read for.
         const bool work = __all_sync(0xffffffffu, more && w.j0 < w.j1);
         ChunkTiles t(w, tpt, wl, wr);
         t.one = __all_sync(0xffffffffu, t.one);
@@ -319,10 +320,10 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
           t.lo[g] = __shfl_sync(0xffffffffu, t.lo[g], 0);
           t.hi[g] = __shfl_sync(0xffffffffu, t.hi[g], 0);
         }
-        // without tiles, one turn for the products that are owed
-        const int last = work ? t.last : t.first + 1;
-        for (int tile = t.first; ok && tile < last; ++tile) {
-          if (work && !t.one && tile > t.first && owed[0] && owed[1] && owed[2] && owed[3] &&
+        const int last = work ? t.last : t.first;
+        const bool owing = (owed[0] | owed[1] | owed[2] | owed[3]) != 0;
+        for (int tile = owing ? t.first - 1 : t.first; ok && tile < last; ++tile) {
+          if (!t.one && tile > t.first && owed[0] && owed[1] && owed[2] && owed[3] &&
               t.in(0, tile) && t.in(1, tile)) {
             const uint32_t v = vi - 1;  // owed by all four
             const uint32_t vs = v % kChunkVStages;
@@ -365,7 +366,6 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
             }
             continue;
           }
-          // an item's first tile: both groups (the item before may have left products owed)
           const bool alone = t.one && tile > t.first;
           bool k_waited = false;
 #pragma unroll 1
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
                 others = others || (k != i && owed[k] != 0 && owed[k] >> 2 == v);
               if (!others) warp_mma_commit(bar(Lay::bVEmpty + vs));
             }
-            if (work && t.in(g, tile)) {
+            if (t.in(g, tile)) {
               if (tile == t.first)
                 ok = warp_wait(bar(Lay::bQFull), static_cast<uint32_t>(item) & 1, abort_flag);
               if (ok && !k_waited) ok = warp_wait(bar(Lay::bKFull + ks), kphase, abort_flag);
@@ -420,7 +420,8 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) owed[k] = k == i ? next : owed[k];
           }
-          if (!ok || !work) break;
+          if (!ok) break;
+          if (tile < t.first) continue;
           warp_mma_commit(bar(Lay::bKEmpty + ks));
           ++vi;
           if (++ks == kChunkKStages) {
@@ -740,7 +741,7 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
           } else {
             __syncwarp();
 #pragma unroll 1
-            for (int e = lane >> 3; e < 32; e += 4) {
+            for (int e = lane >> 3; e < min(32, rows - row0); e += 4) {
               const int row = row0 + e;
               uint4 y;
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
