@@ -181,10 +181,10 @@ bool steps(long long stride, long long rows) { return rows <= 1 || stride > 0; }
 
 // Rows (tokens x query heads of a key head) that the step kernel takes for one pass; the
 // chunk kernel takes more. 24 sequences with 500 to 8000 keys, 32 heads over 8, step and
-// chunk: 17-20 rows 59 and 66 us at d = 128, 20-32 rows 63 and 54 us at d = 64 (a tile there
-// has half the bytes and the same softmax); 36-64 rows 94 and 72 us at d = 128, 88 and 58
-// at d = 64, with a step kernel of 64 columns that these figures took out.
-int step_max_rows(int d) { return d == 128 ? 32 : 16; }
+// chunk: 20 / 24 / 28 / 32 rows 60 / 64 / 67 / 70 and 63 / 64 / 64 / 63 us at d = 128 (the same
+// over 96 sequences of one key head's group of 8: 20 rows 191 and 202, 28 rows 210 and 206),
+// 20-32 rows 63 and 54 us at d = 64 (a tile there has half the bytes and the same softmax).
+int step_max_rows(int d) { return d == 128 ? 24 : 16; }
 
 // Workspace: a PartInfo per CTA, then base-2 log-sum-exps and normalised outputs (fp32) of
 // two parts per CTA, `rows` rows each.

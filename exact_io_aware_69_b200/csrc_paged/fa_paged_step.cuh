@@ -1,5 +1,5 @@
 // fa_paged_step.cuh -- attention of a few new tokens per sequence over a paged cache: the
-// decode step and the check of drafted tokens (up to 32 rows per key head, a row being one
+// decode step and the check of drafted tokens (up to 24 rows per key head, a row being one
 // token's query head).
 //
 // The pass is bound by reading K and V from HBM once: with R rows it does 4 R d

@@ -134,7 +134,7 @@ int fa_paged_append(const fa_paged_append_args *args, void *stream);
  * cache: out [tokens][heads_q][d] and lse [heads_q][tokens] (fp32, natural log). heads_q is
  * a multiple of cache.heads, heads_q / cache.heads <= 128. max_q bounds the new tokens of
  * any sequence (one with more is left out, as above); it picks the kernel: up to 16 rows
- * (tokens x query heads of a key head; 32 at d = 128) are a step, more are a chunk. Work is
+ * (tokens x query heads of a key head; 24 at d = 128) are a step, more are a chunk. Work is
  * shared out evenly over the SMs by key tiles, so a sequence's keys may be split between
  * CTAs; the parts are joined by their log-sum-exps in a fixed order. Results are the same
  * bits on every call with the same lengths (the split, and so the rounding, of a sequence

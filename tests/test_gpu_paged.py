@@ -69,6 +69,8 @@ ATTEND = [  # (lengths, hq, hkv, d, page, window)
     ([(65, 400)], 2, 1, 64, 16, (-1, 40)),
     ([(32, 600), (7, 7)], 1, 1, 128, 16, CAUSAL),
     ([(17, 600), (1, 33)], 1, 1, 64, 16, CAUSAL),
+    ([(24, 600), (7, 7)], 1, 1, 128, 16, CAUSAL),
+    ([(5, 900), (6, 3000)], 8, 2, 128, 32, (700, 0)),
 ]
 
 

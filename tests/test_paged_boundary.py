@@ -167,7 +167,8 @@ def test_workspace_size(lib):
     """Two parts per CTA (148) of 16, 32 or 256 rows, d outputs and a log-sum-exp each, behind
     32 bytes per CTA."""
     for max_q, hq, heads, d, rows in ((1, 8, 8, 64, 16), (4, 32, 8, 128, 16), (5, 32, 8, 128, 32),
-                                      (5, 32, 8, 64, 256), (33, 2, 2, 128, 256)):
+                                      (5, 32, 8, 64, 256), (24, 2, 2, 128, 32),
+                                      (25, 2, 2, 128, 256), (33, 2, 2, 128, 256)):
         assert lib.fa_paged_workspace_size(1000, max_q, hq, heads, d) == \
             148 * 32 + 2 * 148 * rows * (d + 1) * 4
     assert lib.fa_paged_workspace_size(0, 1, 8, 2, 128) == 0
