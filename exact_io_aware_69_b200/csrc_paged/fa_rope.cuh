@@ -17,9 +17,10 @@
 // its token. Threads of a warp run over the heads of a token or over tokens, whichever lie
 // closer together in memory.
 //
-// Small blocks and two rows in flight per thread carry the most bandwidth: 2 x 8192 tokens of 32 + 8 heads, d 128, bf16 (336 MB) take 55.4 us
-// (6.06 TB/s, 0.93 of the copy rate); 256 threads with 2 / 4 / 5 rows 56.2 / 57.6 / 65.2,
-// loading the first rows before the angles are there 57.7 to 65.
+// Small blocks and two rows in flight per thread carry the most bandwidth: 2 x 8192 tokens of
+// 32 + 8 heads, d 128, bf16 (336 MB) take 55.4 us (6.06 TB/s, 0.93 of the copy rate); 256
+// threads with 2 / 4 / 5 rows 56.2 / 57.6 / 65.2, loading the first rows before the angles are
+// there 57.7 to 65.
 #pragma once
 
 #include "fa_paged_common.cuh"
