@@ -156,10 +156,13 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
   constexpr bool kOwn = Roles::kHalves == 2;  // a half of the keys has an O of its own
   // Of every 16 exponential pairs, kPolyPairs go to the FMA pipe: 2048 tokens over 16k keys
   // (32 heads) take 447 / 444 / 431 / 428 us at d = 128 with 0 / 1 / 2 / 4 of them, 310 / 306 /
-  // 331 at d = 64 with 2 / 4 / 8. (Masked scores may take the polynomial: its 2^-125 for them
-  // vanishes next to the row's own weights, and in a row without any nothing is read.)
+  // 331 at d = 64 with 2 / 4 / 8. The polynomial clamps its argument at -125, where it gives
+  // exactly kPolyLeast; that is taken off again, so that a masked score's weight is 0: 2^-125
+  // is a bf16 number, and a large value of a key that the row does not see would show in O.
+  // (A weight above 2^-101 loses nothing by it, others less than 2^-125.)
   constexpr int kPolyPairs = 4;
   constexpr int kPolyStride = 16 / kPolyPairs;
+  constexpr float kPolyLeast = kExp2C0 * 0x1p-125f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t pad = ((raw_base + 1023u) & ~1023u) - raw_base;
@@ -583,6 +586,7 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
               float p0, p1;
               if (i % kPolyStride == kPolyStride - 1) {
                 ex2_poly_pair(x0, x1, p0, p1);
+                f2_unpack(f2_add(f2_pack(p0, p1), f2_pack(-kPolyLeast, -kPolyLeast)), p0, p1);
               } else {
                 p0 = ex2_approx(x0);
                 p1 = ex2_approx(x1);
@@ -647,9 +651,8 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
           for (int i = me + 1; i < me + sharing; ++i) top = fmaxf(top, sums[(i - 1) * 128].x);
         }
       }
-      // Rows that see no key keep the reference -inf, and their sums (which need not be 0: the
-      // polynomial's least value is 2^-125) a factor of 0: O = 0, L = -inf. A NaN among the
-      // scores shows in a sum and stays one.
+      // Rows that see no key keep the reference -inf and sums of 0: O = 0, L = -inf. A NaN
+      // among the scores shows in a sum and stays one.
       const float top_sub = top == -INFINITY ? 0.f : top;
       float inv_l = ex2_approx(m - top_sub);
       if (stores) {
