@@ -555,10 +555,11 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kHeld; i += 8) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mq[k] = fmax3(mq[k], s[i + 2 * k], s[i + 2 * k + 1]);
+              for (int k = 0; k < 4; ++k)
+                mq[k] = fmax3_nan(mq[k], s[i + 2 * k], s[i + 2 * k + 1]);
             }
           }
-          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+          const float mx = fmax3_nan(fmax3_nan(mq[0], mq[1], mq[2]), mq[3], mq[3]);
           const float cand = mx * scale_log2;
           const float m_new = (cand > m + kChunkRescaleSlack) ? cand : m;
           // a row that has seen no key keeps m = -inf: alpha = 1, and 0 is subtracted
@@ -598,7 +599,9 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
           }
           float a0, a1;
           f2_unpack(f2_add(sum2[0], sum2[1]), a0, a1);
-          l = l * alpha + (a0 + a1);
+          // a NaN score comes by the maximum: the polynomial's clamp drops it (NaN weights for the
+          // whole row instead: 449 us where this takes 445, d = 128)
+          l = l * alpha + (isnan(mx) ? mx : a0 + a1);
           // a reference moved, and O holds products: once the last of them has landed (that
           // of the half before; the one before that landed ahead of these scores)
           if ((tile > lo || (!kOwn && h > 0)) && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -652,7 +655,7 @@ __global__ void __launch_bounds__(ChunkRoles<D>::kThreads, 1)
         }
       }
       // Rows that see no key keep the reference -inf and sums of 0: O = 0, L = -inf. A NaN
-      // among the scores shows in a sum and stays one.
+      // among the scores is in the sum and makes O and L NaN.
       const float top_sub = top == -INFINITY ? 0.f : top;
       float inv_l = ex2_approx(m - top_sub);
       if (stores) {

@@ -50,6 +50,12 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedView& c, int b, int max_q
   return s;
 }
 
+// max of three, NaN if any of them is
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
   for (int s = 16; s >= 1; s >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));

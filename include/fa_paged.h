@@ -23,7 +23,8 @@
  * gets O = 0 and L = -inf. V rows of keys that no query of the attention tile at hand sees
  * are never multiplied, whatever they hold, nor are pages that only such keys lie in read.
  * V rows that some of a tile's queries see must be finite (a weight of 0 for the others
- * does not take a NaN or an infinity away); a NaN score makes its own row's O and L NaN.
+ * does not take a NaN or an infinity away); a NaN score, or one of +infinity, makes its own
+ * row's O and L NaN.
  *
  * Lengths, tables and positions are read on the device, so a captured graph follows what
  * they hold when it runs. What the host cannot check is checked there: a sequence whose
