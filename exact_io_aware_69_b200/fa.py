@@ -638,9 +638,9 @@ def paged_attention(q, k_pages, v_pages, page_table, cu_q, seq_k, max_q: int | N
 
 def device_status(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device error word: the first
-    library's, or, where that holds none, the paged library's (if it has been loaded)."""
+    library's, or, where that holds none, the paged library's (if it has been loaded). An
+    error in each is returned by two calls, one after the other."""
     status = int(load().fa_get_device_status(_stream_handle(stream)))
-    if _paged_lib is not None:
-        paged = int(_paged_lib.fa_paged_device_status(_stream_handle(stream)))
-        status = status if status != FA_OK else paged
+    if status == FA_OK and _paged_lib is not None:
+        status = int(_paged_lib.fa_paged_device_status(_stream_handle(stream)))
     return status
