@@ -8,7 +8,9 @@
 // overlaps the attention kernel's, every block finds the rows to join by itself from the
 // CTAs' part records, and the rows are dealt evenly to the blocks: one row to a block and
 // its parts to the warps while there are few rows (a decode step may have a part per SM for
-// each of a handful), else a row to a warp.
+// each of a handful), else a row to a warp. (The parts are written while this kernel is on the
+// device already: their pointers must not be __restrict__ to const, which would allow loads
+// through the cache for data that stays constant.)
 //
 // A part's rows come in tiles of `tile_tokens` tokens, `tile_rows` rows apart; row q of
 // token t of a tile is t * group + q.
@@ -24,10 +26,10 @@ static_assert(kMergeThreads >= kSplitGrid, "one thread per CTA of the split");
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads)
-    fa_paged_merge_kernel(const float* __restrict__ Opart, const float* __restrict__ Lpart,
-                          const PartInfo* __restrict__ parts, int rows_per_slot, int tile_tokens,
-                          int tile_rows, int group, uint16_t* __restrict__ O, Strides so,
-                          float* __restrict__ L, int tokens) {
+    fa_paged_merge_kernel(const float* Opart, const float* Lpart, const PartInfo* parts,
+                          int rows_per_slot, int tile_tokens, int tile_rows, int group,
+                          uint16_t* __restrict__ O, Strides so, float* __restrict__ L,
+                          int tokens) {
   constexpr int CPL = D / 32;
   __shared__ int first_row[kSplitGrid];       // of the item that CTA c began, among all rows
   __shared__ int2 item_of[kSplitGrid];        // its token0 and key head
