@@ -34,6 +34,7 @@ struct SeqInfo {
   int n;      // new tokens
   int nk;     // cached keys, new tokens included
   bool ok;    // the lengths are consistent; otherwise the sequence is left out
+  bool falls; // cu_q decreases: other sequences may claim the same rows
 };
 
 // A sequence's lengths, checked: its rows lie within the packed rows, it has at most max_q
@@ -47,6 +48,7 @@ __device__ __forceinline__ SeqInfo seq_info(const PagedView& c, int b, int max_q
          s.nk >= 0 &&
          s.nk <= (static_cast<long long>(c.table_width) << c.page_shift);
   s.n = s.ok ? end - s.begin : 0;
+  s.falls = end < s.begin;
   return s;
 }
 

@@ -177,7 +177,7 @@ struct Scheduler {
   __device__ __forceinline__ void load(int from) {
     base = from;
     const int i = from + lane;
-    seq = SeqInfo{0, 0, 0, true};
+    seq = SeqInfo{0, 0, 0, true, false};
     if (i < c.batch) seq = seq_info(c, i, max_q);
   }
   __device__ __forceinline__ unsigned cost_of(int place, int n, int nk) const {
@@ -204,22 +204,26 @@ struct Scheduler {
 
   __device__ __forceinline__ void locate(unsigned least) {
     unsigned per_head = 0, own = 0;
+    bool falls = false;
     for (int i = 0; i < c.batch; i += 32) {
       load(i);
+      falls = falls || seq.falls;
       if (!seq.ok && blockIdx.x == 0) atomicExch(&g_fa_status, kStatusInvalid);
       own = seq_cost();
       per_head += __reduce_add_sync(0xffffffffu, own);
     }
-    const unsigned W = per_head * c.heads;
+    // With a cu_q that decreases, the sequences may have more rows than the packed ones, by
+    // which the host has bounded the sums here: nothing is shared out.
+    const unsigned W = __any_sync(0xffffffffu, falls) ? 0 : per_head * c.heads;
     x0 = split_start(W, blockIdx.x, least);
     x1 = split_start(W, blockIdx.x + 1, least);
     at = x0;
     b = c.batch;
     h = p = 0;
     if (x0 >= x1) return;
-    // the sequence that holds x0
+    // the sequence that holds x0 (one does, unless the lengths change meanwhile)
     unsigned before = 0;
-    for (int i = 0;; i += 32) {
+    for (int i = 0; i < c.batch; i += 32) {
       if (c.batch > 32) {
         load(i);
         own = seq_cost();
@@ -250,7 +254,7 @@ struct Scheduler {
   // Sets p to the item of lane l's sequence that holds r; returns the rest.
   __device__ __forceinline__ unsigned locate_item(int l, unsigned r) {
     const int n = __shfl_sync(0xffffffffu, seq.n, l), nk = __shfl_sync(0xffffffffu, seq.nk, l);
-    for (int i = lane;; i += 32) {  // ends: r is below the sum over all items
+    for (int i = lane; (i - lane) * tpi < n; i += 32) {  // finds it: r is below the sum
       unsigned sum = i * tpi < n ? cost_of(i, n, nk) : 0;
       const unsigned cost = sum;
 #pragma unroll
@@ -266,6 +270,7 @@ struct Scheduler {
       }
       r -= __shfl_sync(0xffffffffu, sum, 31);
     }
+    return 0;
   }
 
   __device__ __forceinline__ void run(ItemRing& ring, volatile int* abort_flag, PartInfo* parts) {
@@ -288,7 +293,7 @@ struct Scheduler {
           it.j0 = at < x0 ? split_tile(x0 - at, kStart) : 0;
           it.j1 = at + cost <= x1 ? it.keys.count : split_tile(x1 - at, kStart);
           if (it.j1 > it.j0 || (it.keys.count == 0 && at + cost <= x1)) {
-            if (it.j1 < it.keys.count) {  // a later CTA goes on with it
+            if (it.j1 < it.keys.count && blockIdx.x + 1 < kSplitGrid) {  // a later CTA goes on
               info.goes_on = it.j0 > 0;
               info.begins = it.j0 == 0;
               info.token0 = it.begin + p * tpi;

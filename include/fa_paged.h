@@ -29,8 +29,9 @@
  * Lengths, tables and positions are read on the device, so a captured graph follows what
  * they hold when it runs. What the host cannot check is checked there: a sequence whose
  * lengths are inconsistent (cu_q decreasing or above the packed rows, more keys than the
- * table's width holds, fewer keys than new tokens in an append) is left out, and a page
- * index outside [0, num_pages) reads as zeros and is not written; either makes the next
+ * table's width holds, fewer keys than new tokens in an append) is left out, by an attention
+ * the whole batch if cu_q decreases anywhere (rows might belong to two sequences), and a page
+ * index outside [0, num_pages) reads as zeros and is not written; each makes the next
  * fa_paged_device_status return FA_ERR_INVALID.
  *
  * Pointers are device pointers of the current device, 16-byte aligned (4 for the 32-bit

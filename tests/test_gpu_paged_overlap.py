@@ -31,3 +31,18 @@ def test_calls_in_a_row_share_a_workspace(shapes):
     assert fa.device_status() == fa.FA_OK
     for i, (o, L) in got:
         assert torch.equal(o, wants[i][0]) and torch.equal(L, wants[i][1])
+
+
+@pytest.mark.parametrize("n", [1, 50])
+def test_a_decreasing_cu_q_leaves_the_batch_out(n):
+    """Rows might belong to two sequences: none is written, and the status says so."""
+    import torch
+    batch = make_batch([(n, 300), (n, 200), (n, 700)], 4, 2, 128, 64, torch.bfloat16, seed=5)
+    for cu in ([0, n, n - 1, 3 * n], [0, 3 * n, 0, 3 * n], [n, 0, 2 * n, 3 * n]):
+        out = torch.full_like(batch.q, 7.0)
+        lse = torch.full((4, 3 * n), 7.0, device="cuda")
+        fa.paged_attention(batch.q, batch.k_pages, batch.v_pages, batch.page_table,
+                           torch.tensor(cu, dtype=torch.int32, device="cuda"), batch.seq_k,
+                           max_q=3 * n, out=out, lse=lse)
+        assert fa.device_status() == fa.FA_ERR_INVALID
+        assert (out == 7).all() and (lse == 7).all()
