@@ -81,8 +81,26 @@ int launch_rope(fa::RopeArgs& a, bool interleaved, int dtype, cudaStream_t strea
                 grid, fa::kRopeThreads, smem, stream, a, interleaved);
 }
 
-bool ok_rows(const fa_rope_rows& r) {
-  return r.heads == 0 || (ok_ptr(r.x) && ok_ptr(r.y) && ok_strides(r.xs) && ok_strides(r.ys));
+// A stride of 0 over more than one row aliases rows: no tensor map describes them, and
+// writing them would leave whichever came last.
+bool steps(long long stride, long long rows) { return rows <= 1 || stride > 0; }
+bool cache_steps(const fa_paged_cache& c) {
+  return steps(c.k_row, c.page_size) && steps(c.k_head, c.heads) && steps(c.k_page, c.num_pages) &&
+         steps(c.v_row, c.page_size) && steps(c.v_head, c.heads) && steps(c.v_page, c.num_pages);
+}
+
+// Rows of heads to rotate, `n` of each of `batch`. In place the strides have to be the same:
+// a thread reads the columns of a row that it writes, before it writes them, and no others.
+int check_rows(const fa_rope_rows& r, int batch, int n) {
+  if (r.heads == 0) return FA_OK;
+  if (!ok_ptr(r.x) || !ok_ptr(r.y) || !ok_strides(r.xs) || !ok_strides(r.ys))
+    return FA_ERR_INVALID;
+  if (!steps(r.ys.b, batch) || !steps(r.ys.h, r.heads) || !steps(r.ys.n, n))
+    return FA_ERR_UNSUPPORTED;
+  if (r.x == r.y && ((batch > 1 && r.xs.b != r.ys.b) || (r.heads > 1 && r.xs.h != r.ys.h) ||
+                     (n > 1 && r.xs.n != r.ys.n)))
+    return FA_ERR_INVALID;
+  return FA_OK;
 }
 fa::RopeRows rope_rows(const fa_rope_rows& r) {
   return {static_cast<const uint16_t*>(r.x), static_cast<uint16_t*>(r.y), strides(r.xs),
@@ -176,9 +194,6 @@ bool make_part_tmap(CUtensorMap* map, const float* ptr, int d, int rows) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// A stride of 0 over more than one row would alias rows of a tensor map.
-bool steps(long long stride, long long rows) { return rows <= 1 || stride > 0; }
-
 // Rows (tokens x query heads of a key head) that the step kernel takes for one pass; the
 // chunk kernel takes more. 24 sequences with 500 to 8000 keys, 32 heads over 8, step and
 // chunk: 20 / 24 / 28 / 32 rows 60 / 64 / 67 / 70 and 63 / 64 / 64 / 63 us at d = 128 (the same
@@ -327,10 +342,12 @@ int fa_rope(const fa_rope_args* args, void* stream) {
     return FA_ERR_INVALID;
   if (r.dtype != FA_BF16 && r.dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
   if (r.d % 16 != 0 || r.d > fa::kRopeMaxDim) return FA_ERR_UNSUPPORTED;
-  const int st = check_rotation(r.d, r.rot_dim, r.magnitude, r.freqs);
+  int st = check_rotation(r.d, r.rot_dim, r.magnitude, r.freqs);
   if (st != FA_OK) return st;
   if (static_cast<long long>(r.batch) * r.rows == 0 || r.q.heads + r.k.heads == 0) return FA_OK;
-  if (!ok_rows(r.q) || !ok_rows(r.k) || !aligned(r.positions, 4)) return FA_ERR_INVALID;
+  if ((st = check_rows(r.q, r.batch, r.rows)) != FA_OK) return st;
+  if ((st = check_rows(r.k, r.batch, r.rows)) != FA_OK) return st;
+  if (!aligned(r.positions, 4)) return FA_ERR_INVALID;
   fa::RopeArgs a{};
   a.kinds[0] = rope_rows(r.q);
   a.kinds[1] = rope_rows(r.k);
@@ -357,10 +374,12 @@ int fa_paged_append(const fa_paged_append_args* args, void* stream) {
       (st = check_rotation(c.d, r.rot_dim, r.magnitude, r.freqs)) != FA_OK)
     return st;
   if (c.batch == 0 || c.tokens == 0) return FA_OK;
-  if (!ok_ptr(r.k) || !ok_ptr(r.v) || !ok_strides(r.ks) || !ok_strides(r.vs) || !ok_rows(r.q) ||
+  if (!ok_ptr(r.k) || !ok_ptr(r.v) || !ok_strides(r.ks) || !ok_strides(r.vs) ||
       !aligned(r.positions, 4))
     return FA_ERR_INVALID;
+  if ((st = check_rows(r.q, 1, c.tokens)) != FA_OK) return st;
   if (c.num_pages == 0 || c.table_width == 0) return FA_ERR_INVALID;
+  if (!cache_steps(c)) return FA_ERR_UNSUPPORTED;
   const fa_strides kp{c.k_page, c.k_head, c.k_row}, vp{c.v_page, c.v_head, c.v_row};
   fa::RopeArgs a{};
   a.kinds[0] = rope_rows(r.q);
@@ -401,9 +420,7 @@ int fa_paged_attention(const fa_paged_attention_args* args, void* stream) {
     return FA_ERR_INVALID;
   if (c.num_pages == 0 || c.table_width == 0) return FA_ERR_INVALID;
   if (!steps(r.qs.h, r.heads_q) || !steps(r.qs.n, c.tokens) || !steps(r.os.h, r.heads_q) ||
-      !steps(r.os.n, c.tokens) || !steps(c.k_row, c.page_size) || !steps(c.k_head, c.heads) ||
-      !steps(c.k_page, c.num_pages) || !steps(c.v_row, c.page_size) ||
-      !steps(c.v_head, c.heads) || !steps(c.v_page, c.num_pages))
+      !steps(r.os.n, c.tokens) || !cache_steps(c))
     return FA_ERR_UNSUPPORTED;
   const int max_q = r.max_q < c.tokens ? r.max_q : c.tokens;
   // the split counts key tiles of items in 32 bits

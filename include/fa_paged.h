@@ -47,8 +47,9 @@
  * scales, magnitudes or rotation sizes, a workspace that is too small; FA_ERR_UNSUPPORTED
  * for dtypes, head dims, page sizes and group sizes other than named below, more than 8192
  * sequences, 1024 key heads or 2^28 packed rows or keys per sequence, a stride of 0 over
- * more than one row in an attention, or a batch of 2^31 and more (item, key tile) pairs by
- * its bounds (tokens, batch, table_width); FA_ERR_CUDA when CUDA refuses a launch.
+ * more than one row in an attention or in what a call writes, or a batch of 2^31 and more
+ * (item, key tile) pairs by its bounds (tokens, batch, table_width); FA_ERR_CUDA when CUDA
+ * refuses a launch.
  */
 #ifndef FA_PAGED_H_
 #define FA_PAGED_H_
@@ -96,7 +97,7 @@ typedef struct {
  * `inverse` = 1 turns by -a instead, which is the gradient of the rotation (same
  * magnitude). Row n of batch b is at positions[b * pos_row + n] (pos_row = 0: the same for
  * every batch), or at n when positions is NULL. y may be x with the same strides (in
- * place); otherwise they must not overlap. d and rot_dim are multiples of 16,
+ * place; FA_ERR_INVALID with others); otherwise they must not overlap. d and rot_dim are multiples of 16,
  * 16 <= rot_dim <= d <= 1024.
  */
 typedef struct {
