@@ -33,7 +33,7 @@ def set_values(batch, b, keys, value):
     (4, 4, 2, (-1, 0)),
 ])
 def test_values_outside_a_rows_mask(n, group, first, window, d, dtype):
-    """Eight neighbouring new tokens (fewer for short drafts) with the type's largest values:
+    """Sixteen neighbouring new tokens (fewer for short drafts) with the type's largest values:
     rows that see none of them are within the bounds of the definition. (Those that see
     them may pass the type's range.)"""
     import torch
@@ -41,7 +41,7 @@ def test_values_outside_a_rows_mask(n, group, first, window, d, dtype):
     batch = make_batch(lengths, 2 * group, 2, d, 32, getattr(torch, dtype), seed=n + d)
     rows = torch.arange(n, device="cuda")
     left = n if window[0] < 0 else window[0]
-    last = min(first + 8, n)
+    last = min(first + 16, n)
     blind = (rows + window[1] < first) | (rows - left >= last)
     assert blind.any() and not blind.all()
     for b, (_, k) in enumerate(lengths):

@@ -30,14 +30,14 @@ def seen(n, keys, key):
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("n,group,keys", CASES)
 def test_a_nan_key_at_every_place(n, group, keys, d):
-    """One NaN key at a time: eight neighbouring places in each half of the last whole tile,
+    """One NaN key at a time: sixteen neighbouring places in each half of the last whole tile,
     and among the new tokens."""
     import torch
     batch = make_batch([(n, keys), (n, keys)], 2 * group, 2, d, 64, torch.bfloat16, seed=n)
     plain, plain_l = fa.paged_attention(batch.q, *batch.cache, max_q=n)
     tile = (keys // 128 - 1) * 128
-    places = list(range(tile + 24, tile + 32)) + list(range(tile + 88, tile + 96))
-    places += range(max(0, keys - n), min(keys, keys - n + 8))
+    places = list(range(tile + 16, tile + 32)) + list(range(tile + 80, tile + 96))
+    places += range(max(0, keys - n), min(keys, keys - n + 16))
     for key in places:
         row = key_row(batch, 1, key, 0)
         old = row.clone()
@@ -82,7 +82,7 @@ def test_an_infinite_key_at_every_place(n, group, keys, d):
     column = batch.q[:, :, 9]
     column[column == 0] = 0.5  # infinity times 0 is not a number
     tile = (keys // 128 - 1) * 128
-    for key in list(range(tile + 24, tile + 32)) + list(range(tile + 88, tile + 96)):
+    for key in list(range(tile + 16, tile + 32)) + list(range(tile + 80, tile + 96)):
         row = key_row(batch, 0, key, 0)
         old = row.clone()
         row.zero_()
