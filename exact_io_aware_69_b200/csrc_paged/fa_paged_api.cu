@@ -196,8 +196,8 @@ bool make_part_tmap(CUtensorMap* map, const float* ptr, int d, int rows) {
 }
 // Rows (tokens x query heads of a key head) that the step kernel takes for one pass; the
 // chunk kernel takes more. 24 sequences with 500 to 8000 keys, 32 heads over 8, step and
-// chunk: 20 / 24 / 28 / 32 rows 60 / 64 / 67 / 70 and 63 / 64 / 64 / 63 us at d = 128 (the same
-// over 96 sequences of one key head's group of 8: 20 rows 191 and 202, 28 rows 210 and 206),
+// chunk: 20 / 24 / 28 / 32 rows 60 / 64 / 67 / 70 and 64 / 64 / 64 / 64 us at d = 128 (96
+// sequences, a key head for each query head: 20 rows 194 and 210, 28 rows 212 and 212),
 // 20-32 rows 63 and 54 us at d = 64 (a tile there has half the bytes and the same softmax).
 int step_max_rows(int d) { return d == 128 ? 24 : 16; }
 

@@ -26,8 +26,8 @@ constexpr int kKeyTile = 128;
 // Starting and finishing an item in key tiles' time: its first scores wait for its first
 // keys, and its last product is followed by the sums and the store. 64 single tokens over
 // 300 to 16,384 keys take 160 / 163 / 165 us with 2 / 3 / 4; prompts of 100 to 2000 tokens
-// with and without single tokens 77.7 / 75.6 / 73.4 and 116 / 104 / 108 us (d = 64),
-// 124 / 117 / 119 and 152 / 136 / 137 (d = 128).
+// with and without single tokens 73.7 / 73.9 / 72.2 and 113 / 103 / 107 us (d = 64),
+// 117 / 115 / 118 and 135 / 130 / 136 (d = 128).
 constexpr int kStepItemCost = 2;
 constexpr int kChunkItemCost = 3;
 

@@ -143,8 +143,11 @@ int fa_paged_append(const fa_paged_append_args *args, void *stream);
  * bits on every call with the same lengths (the split, and so the rounding, of a sequence
  * depends on the lengths of the others). The weights are rounded to the 16-bit type for
  * their product with V, relative to about the largest so far: in fp16 those below 2^-14 of
- * it lose digits and those below 2^-25 vanish. The workspace is 256-byte aligned; its
- * contents do not matter. Two launches.
+ * it lose digits and those below 2^-25 vanish. A step divides the product by the sum of the
+ * rounded weights, a chunk by that of the unrounded ones: there the rounding of a weight that
+ * dominates its row stays in O, up to half a step of its key's value, and weights that
+ * vanish still count in the sum. With max_q = 0 nothing is done. The workspace is 256-byte
+ * aligned; its contents do not matter. Two launches.
  */
 typedef struct {
     fa_paged_cache cache;
